@@ -305,6 +305,112 @@ kv4_status kv4_bf16_decode_attn(kv4_cache* cache, int layer, int B, const void* 
                                 size_t ws_bytes, void* stream);
 
 /*
+ * Rotary positions up to the cache.  Between a model's query/key/value projection and the decode lie
+ * the per-head norms of the queries and keys, the rotation of both by their position, and the append.
+ *
+ * The rotation turns pair i (0 <= i < R/2) of a head at position p by the angle p f_i:
+ * (a, b) -> (a cos - b sin, b cos + a sin), (a, b) = elements (i, i + R/2) with KV4_ROPE_HALF or
+ * (2i, 2i + 1) with KV4_ROPE_INTERLEAVED; elements past rotary_dim = R stay as they are.  f_i =
+ * base^(-2i/R), scaled for contexts beyond the trained length by
+ *   KV4_ROPE_SCALE_LINEAR  f_i / factor (positions interpolated);
+ *   KV4_ROPE_SCALE_NTK     base^(-2i/R) with base * factor^(R / (R - 2));
+ *   KV4_ROPE_SCALE_YARN    ("YaRN: Efficient Context Window Extension of Large Language Models",
+ *                          section 3.2): pairs that turn at least beta_fast times over
+ *                          original_max_pos keep f_i, at most beta_slow times take f_i / factor, a
+ *                          linear ramp over the pair index between; cos and sin are multiplied by
+ *                          attention_factor (0: 0.1 ln(factor) + 1 when factor > 1);
+ *   KV4_ROPE_SCALE_BANDS   pairs that turn at least high_freq_factor times over original_max_pos
+ *                          keep f_i, at most low_freq_factor times take f_i / factor, a blend that is
+ *                          linear in the number of turns between.
+ * Fields that a scaling does not name are not read; attention_factor 0 means 1 for the others.
+ */
+#define KV4_ROPE_HALF 0
+#define KV4_ROPE_INTERLEAVED 1
+#define KV4_ROPE_SCALE_NONE 0
+#define KV4_ROPE_SCALE_LINEAR 1
+#define KV4_ROPE_SCALE_NTK 2
+#define KV4_ROPE_SCALE_YARN 3
+#define KV4_ROPE_SCALE_BANDS 4
+
+typedef struct {
+  int rotary_dim;         /* R: a multiple of 8, 8..128                       */
+  int max_pos;            /* positions of the table                           */
+  int scaling;            /* KV4_ROPE_SCALE_*                                 */
+  int original_max_pos;   /* KV4_ROPE_SCALE_YARN, _BANDS: the trained length  */
+  double base;            /* > 1                                              */
+  double factor;          /* > 0                                              */
+  double low_freq_factor, high_freq_factor; /* KV4_ROPE_SCALE_BANDS, 0 < low < high  */
+  double beta_fast, beta_slow;              /* KV4_ROPE_SCALE_YARN, fast > slow > 0  */
+  double attention_factor;
+} kv4_rope_config;
+
+/*
+ * kv4_rope_table: write the table the calls below read, fp32 [max_pos][R/2][2] (cos, sin), each entry
+ * the fp64 value (of the angle p f_i taken in fp64) rounded once.  table: device, 16-byte aligned,
+ * max_pos * R * 4 bytes.  A program builds it once; a caller's own table of that form serves as well.
+ */
+kv4_status kv4_rope_table(const kv4_rope_config* cfg, float* table, void* stream);
+
+/* A table with the norms: head vector x becomes x r w, r = 1 / sqrt(mean of x^2 + eps), before the
+ * rotation; a NULL weight leaves that norm out.  The sum of squares is taken in fp64, r rounded to
+ * fp32, everything after it in fp32, rounded once to the output's type. */
+typedef struct {
+  const float* table;      /* device fp32 [max_pos][rotary_dim / 2][2], 16-byte aligned    */
+  int max_pos;
+  int rotary_dim;          /* a multiple of 8, at most head_dim                            */
+  int layout;              /* KV4_ROPE_HALF or KV4_ROPE_INTERLEAVED                        */
+  kv4_dtype weight_dtype;  /* of both weights                                              */
+  const void* q_weight;    /* device [head_dim] or NULL                                    */
+  const void* k_weight;    /* device [head_dim] or NULL                                    */
+  float eps;               /* >= 0                                                         */
+} kv4_rope_params;
+
+/*
+ * kv4_rope: norm and rotate T tokens' queries and keys without a cache (for attention over the
+ * tokens themselves, or for kv4_allocate_key_bits, which scores rotated keys).  q [T][Hq][D] and
+ * k [T][Hkv][D] of any kv4_dtype, the heads of a token contiguous, tokens *_stride elements apart
+ * (so slices of a fused projection serve as they are); the outputs likewise, in their own types,
+ * and either output may be its input (same type and stride).  Hq or Hkv may be 0 (that side's
+ * pointers are not read).  Pointers are 16-byte (fp32) or 8-byte aligned and strides multiples of
+ * 4.  pos: device int32 [T]; a row with pos -1 is padding: its outputs are left as they were.  A
+ * position outside [0, max_pos) otherwise sets KV4_DEVERR_LENGTH and is left out too.
+ */
+kv4_status kv4_rope(const kv4_rope_params* rope, int T, int Hq, int Hkv, int D, const void* q, kv4_dtype q_dtype,
+                    int64_t q_stride, const void* k, kv4_dtype k_dtype, int64_t k_stride, const int32_t* pos,
+                    void* q_out, kv4_dtype q_out_dtype, int64_t q_out_stride, void* k_out, kv4_dtype k_out_dtype,
+                    int64_t k_out_stride, void* stream);
+
+/*
+ * kv4_append_rope: kv4_append (any cache handle, the BF16 baseline's included) of keys that are
+ * normed and rotated on the way, together with the queries of the same tokens: q_out receives what
+ * kv4_rope would write, the cache what kv4_append would store of kv4_rope's fp32 keys, bit for bit,
+ * and the rotated keys never reach memory.  Types, strides and alignment as for kv4_rope (K and V
+ * may be fp16 as well here); q NULL appends only.  The position of a token is pos[t] for the
+ * rotation and the cache alike; a row with seq_slot -1 is padding: nothing of it is written.
+ * Device-side checks as for kv4_append, and a position of max_pos or more sets KV4_DEVERR_LENGTH;
+ * nothing of such a token is written, its q_out row included.
+ */
+kv4_status kv4_append_rope(kv4_cache* cache, int layer, int T, const kv4_rope_params* rope, const void* q,
+                           kv4_dtype q_dtype, int64_t q_stride, const void* K, kv4_dtype k_dtype, int64_t k_stride,
+                           const void* V, kv4_dtype v_dtype, int64_t v_stride, const int32_t* seq_slot,
+                           const int32_t* pos, const int32_t* lens_after, const int32_t* page_table, int stride,
+                           void* q_out, kv4_dtype q_out_dtype, int64_t q_out_stride, void* stream);
+
+/*
+ * kv4_gather: read T cached positions (seq_slot[t], pos[t]) of one layer back as dense keys and
+ * values [T][Hkv][D] of out_dtype in their original basis (the stored rotation undone), for example
+ * the earlier context of a chunked prefill.  Any cache handle.  With lens (device int32
+ * [max_seqs]) a position that a decode at lens[slot] reads from the INT8 side cache comes from
+ * there, and one at or past lens[slot] sets KV4_DEVERR_LENGTH; NULL reads every position from the
+ * pages.  K_out or V_out may be NULL; both are 16-byte aligned.  Rows with seq_slot -1, and rows that
+ * set an error bit (as for kv4_append), are left as they were.  Values are scale and zero applied
+ * in fp32, rounded once.
+ */
+kv4_status kv4_gather(kv4_cache* cache, int layer, int T, const int32_t* seq_slot, const int32_t* pos,
+                      const int32_t* lens, const int32_t* page_table, int stride, void* K_out, void* V_out,
+                      kv4_dtype out_dtype, void* stream);
+
+/*
  * kv4_decode_attn_static: kv4_decode_attn for callers that cannot allocate device memory -- code
  * running inside another runtime's memory pool that forbids foreign allocations, a serving
  * process that reserved all device memory up front for its page pools, or a caller that has no

@@ -3,11 +3,12 @@
   libkv4.so     the INT4 KV cache library (C ABI in include/kv4.h)
   libkv4gen.so  the GPU twin of the seeded input generator (tests and benchmark only)
 
-Run ``python -m int4_kv_cache_append_b200.build`` (or ``__graft_entry__.build()``).  Objects are
-rebuilt only when a source or header is newer than the library.
+Run ``python -m int4_kv_cache_append_b200.build`` (or ``__graft_entry__.build()``).  Sources
+compile in parallel; a library is rebuilt only when a source or header is newer than it.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import subprocess
@@ -18,11 +19,11 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
-COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-shared", "-ftz=false", "-prec-div=true", "-prec-sqrt=true",
+COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-ftz=false", "-prec-div=true", "-prec-sqrt=true",
           "-Xptxas", "-v"]
 
 LIBS = {
-    "libkv4.so": ["kv4_api.cu", "kv4_append.cu", "kv4_decode.cu", "kv4_bf16.cu", "kv4_mixed.cu"],
+    "libkv4.so": ["kv4_api.cu", "kv4_append.cu", "kv4_decode.cu", "kv4_bf16.cu", "kv4_mixed.cu", "kv4_rope.cu"],
     "libkv4gen.so": ["kv4gen.cu"],
 }
 
@@ -43,13 +44,22 @@ def build(force: bool = False, verbose: bool = False) -> dict[str, str]:
         src_paths = [os.path.join(CSRC, s) for s in srcs]
         if force or _stale(target, src_paths + headers):
             tmp = target + f".tmp{os.getpid()}"
-            cmd = [NVCC, *ARCH, *COMMON, "-I", os.path.join(ROOT, "include"), "-o", tmp, *src_paths]
-            r = subprocess.run(cmd, capture_output=True, text=True)
-            if r.returncode != 0:
-                sys.stderr.write(r.stdout + r.stderr)
+            objs = [tmp + "." + os.path.basename(s) + ".o" for s in src_paths]
+            cmds = [[NVCC, *ARCH, *COMMON, "-I", os.path.join(ROOT, "include"), "-c", "-o", o, s] for o, s in zip(objs, src_paths)]
+            try:
+                with concurrent.futures.ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:
+                    runs = list(pool.map(lambda c: subprocess.run(c, capture_output=True, text=True), cmds))
+                if all(r.returncode == 0 for r in runs):
+                    runs.append(subprocess.run([NVCC, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True))
+            finally:
+                for o in objs:
+                    if os.path.exists(o):
+                        os.remove(o)
+            if any(r.returncode != 0 for r in runs):
+                sys.stderr.write("".join(r.stdout + r.stderr for r in runs if r.returncode != 0))
                 raise RuntimeError(f"nvcc failed for {lib}")
             if verbose:
-                sys.stderr.write(r.stderr)
+                sys.stderr.write("".join(r.stderr for r in runs))
             os.replace(tmp, target)
         out[lib] = target
     return out

@@ -157,6 +157,41 @@ size_t workspace_for(const kv4_cache* c, int B, int ctas) {
 // bit-width key cache (a BF16 baseline handle maps to FMT_INT4 and is then rejected).
 int own_format(const kv4_cache* c) { return (c && c->format == FMT_MIXED) ? FMT_MIXED : FMT_INT4; }
 
+// Everything of AppendArgs that comes from the cache, the layer and the token lists.
+kv4::AppendArgs cache_args(const kv4_cache* c, int layer, int T, const int32_t* seq_slot, const int32_t* pos,
+                           const int32_t* lens_after, const int32_t* page_table, int stride, uint32_t* err) {
+  const bool int4 = c->format == FMT_INT4;
+  kv4::AppendArgs a{};
+  a.pool = c->pool + static_cast<size_t>(layer) * c->pool_layer_bytes;
+  a.side = c->side ? c->side + static_cast<size_t>(layer) * c->side_layer_bytes : nullptr;
+  a.seq_slot = seq_slot;
+  a.pos = pos;
+  a.lens_after = lens_after;
+  a.page_table = page_table;
+  a.stride = stride;
+  a.T = T;
+  a.Hkv = c->cfg.num_kv_heads;
+  a.P = c->cfg.page_size;
+  a.s = int4 ? c->cfg.num_sinks : 0;
+  a.w = int4 ? c->cfg.recent_window : 0;
+  a.h = int4 ? c->cfg.hadamard_block : 1;
+  a.max_seqs = c->cfg.max_seqs;
+  a.max_pages = c->cfg.max_pages;
+  a.nt8 = c->nt8;
+  a.page_bytes = c->page_bytes;
+  a.side_slot_bytes = c->side_slot_bytes;
+  for (int i = 0; i < 4; ++i) a.signs[i] = int4 ? c->signs[i] : 0u;
+  a.rotate_v = int4 ? c->rotate_v : 0;
+  a.vbf = (int4 && c->cfg.value_format == KV4_VALUES_BF16) ? 1 : 0;
+  if (c->format == FMT_MIXED) {
+    a.alloc = c->alloc_base + static_cast<size_t>(layer) * c->alloc_layer_bytes;
+    a.kbits = c->cfg.key_bits;
+    a.vbits = c->cfg.value_bits;
+  }
+  a.err = err;
+  return a;
+}
+
 kv4_status append_common(kv4_cache* c, int fmt, int layer, int T, const void* K, kv4_dtype kd, const void* V,
                          kv4_dtype vd, const int32_t* seq_slot, const int32_t* pos, const int32_t* lens_after,
                          const int32_t* page_table, int stride, void* stream) {
@@ -170,44 +205,53 @@ kv4_status append_common(kv4_cache* c, int fmt, int layer, int T, const void* K,
   if (static_cast<long long>(T) * c->cfg.num_kv_heads > (1LL << 30)) return KV4_ERR_UNSUPPORTED;
   uint32_t* err = nullptr;
   if (!device_info(&err, nullptr)) return KV4_ERR_CUDA;
-  kv4::AppendArgs a{};
-  a.pool = c->pool + static_cast<size_t>(layer) * c->pool_layer_bytes;
-  a.side = c->side ? c->side + static_cast<size_t>(layer) * c->side_layer_bytes : nullptr;
+  kv4::AppendArgs a = cache_args(c, layer, T, seq_slot, pos, lens_after, page_table, stride, err);
   a.K = K;
   a.V = V;
   a.k_dtype = kd;
   a.v_dtype = vd;
-  a.seq_slot = seq_slot;
-  a.pos = pos;
-  a.lens_after = lens_after;
-  a.page_table = page_table;
-  a.stride = stride;
-  a.T = T;
-  a.Hkv = c->cfg.num_kv_heads;
-  a.P = c->cfg.page_size;
-  a.s = c->cfg.num_sinks;
-  a.w = c->cfg.recent_window;
-  a.h = c->cfg.hadamard_block;
-  a.max_seqs = c->cfg.max_seqs;
-  a.max_pages = c->cfg.max_pages;
-  a.nt8 = c->nt8;
-  a.page_bytes = c->page_bytes;
-  a.side_slot_bytes = c->side_slot_bytes;
-  for (int i = 0; i < 4; ++i) a.signs[i] = fmt == FMT_INT4 ? c->signs[i] : 0u;
-  a.rotate_v = fmt == FMT_INT4 ? c->rotate_v : 0;
-  a.vbf = (fmt == FMT_INT4 && c->cfg.value_format == KV4_VALUES_BF16) ? 1 : 0;
-  if (fmt == FMT_MIXED) {
-    a.alloc = c->alloc_base + static_cast<size_t>(layer) * c->alloc_layer_bytes;
-    a.kbits = c->cfg.key_bits;
-    a.vbits = c->cfg.value_bits;
-  }
-  a.err = err;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = fmt == FMT_INT4    ? kv4::launch_append_int4(a, c->cfg.head_dim, st)
                         : fmt == FMT_MIXED ? kv4::launch_append_mixed(a, c->cfg.head_dim, st)
                                            : kv4::launch_append_bf16(a, c->cfg.head_dim, st);
   return e == cudaSuccess ? KV4_OK : KV4_ERR_CUDA;
 }
+
+// Rows of D-element heads, `stride` elements apart: the kernels move four elements at a time.
+bool rows_ok(const void* p, kv4_dtype d, int64_t stride, int64_t row) {
+  return p && dtype_ok_q(d) == KV4_OK && aligned(p, d == KV4_F32 ? 16 : 8) && stride >= row && stride % 4 == 0;
+}
+
+kv4_status check_rope(const kv4_rope_params* r, int D) {
+  if (!r || !r->table || !aligned(r->table, 16) || r->max_pos <= 0 || !(r->eps >= 0.f) || !std::isfinite(r->eps))
+    return KV4_ERR_INVALID_ARG;
+  if (r->layout != KV4_ROPE_HALF && r->layout != KV4_ROPE_INTERLEAVED) return KV4_ERR_INVALID_ARG;
+  if (r->rotary_dim <= 0 || r->rotary_dim > D) return KV4_ERR_INVALID_ARG;
+  if (r->rotary_dim % 8) return KV4_ERR_UNSUPPORTED;
+  if (r->q_weight || r->k_weight) {
+    if (dtype_ok_q(r->weight_dtype) != KV4_OK) return KV4_ERR_INVALID_ARG;
+    const size_t al = r->weight_dtype == KV4_F32 ? 16 : 8;
+    if (!aligned(r->q_weight, al) || !aligned(r->k_weight, al)) return KV4_ERR_INVALID_ARG;
+  }
+  return KV4_OK;
+}
+
+kv4::RopeArgs rope_args(const kv4_rope_params* r, uint32_t* err) {
+  kv4::RopeArgs a{};
+  a.table = r->table;
+  a.max_pos = r->max_pos;
+  a.R = r->rotary_dim;
+  a.layout = r->layout;
+  a.qw = r->q_weight;
+  a.kw = r->k_weight;
+  a.w_dtype = r->weight_dtype;
+  a.eps = static_cast<double>(r->eps);
+  a.err = err;
+  return a;
+}
+
+// Warps of the rotary kernels are counted in 32 bits.
+constexpr long long kMaxVectors = 1LL << 26;
 
 kv4_status decode_common(kv4_cache* c, int fmt, int layer, int B, const void* q, kv4_dtype qd,
                          const int32_t* page_table, int stride, const int32_t* lens, int max_len_hint, float* out,
@@ -551,6 +595,155 @@ kv4_status kv4_bf16_decode_attn(kv4_cache* cache, int layer, int B, const void* 
                                 float* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
   return decode_common(cache, FMT_BF16, layer, B, q, q_dtype, page_table, stride, lens, max_len_hint, out, lse,
                        workspace, ws_bytes, stream);
+}
+
+// Frequencies of a rotary configuration as turns per position; false when a parameter is out of range.
+static bool rope_frequencies(const kv4_rope_config* c, double* turns, double* mult) {
+  constexpr double kTwoPi = 6.283185307179586476925;
+  auto positive = [](double x) { return x > 0.0 && std::isfinite(x); };
+  const int R = c->rotary_dim, n = R / 2;
+  const double f = c->factor, L = static_cast<double>(c->original_max_pos);
+  if (!(c->base > 1.0) || !std::isfinite(c->base) || !std::isfinite(c->attention_factor) || c->attention_factor < 0.0) return false;
+  if (c->scaling != KV4_ROPE_SCALE_NONE && !positive(f)) return false;
+  *mult = c->attention_factor > 0.0 ? c->attention_factor : 1.0;
+  const double base = c->scaling == KV4_ROPE_SCALE_NTK ? c->base * std::pow(f, static_cast<double>(R) / (R - 2)) : c->base;
+  if (!(base > 0.0) || !std::isfinite(base)) return false;
+  double low = 0.0, high = 1.0;
+  if (c->scaling == KV4_ROPE_SCALE_YARN) {
+    if (c->original_max_pos <= 0 || !positive(c->beta_slow) || !positive(c->beta_fast) || c->beta_fast <= c->beta_slow) return false;
+    // pair index at which a pair turns `beta` times over the trained length
+    auto index = [&](double beta) { return R * std::log(L / (beta * kTwoPi)) / (2.0 * std::log(c->base)); };
+    low = std::fmax(std::floor(index(c->beta_fast)), 0.0);
+    high = std::fmin(std::ceil(index(c->beta_slow)), R - 1.0);
+    if (!(high > low)) high = low + 0.001;
+    if (c->attention_factor == 0.0 && f > 1.0) *mult = 0.1 * std::log(f) + 1.0;
+  }
+  if (c->scaling == KV4_ROPE_SCALE_BANDS &&
+      (c->original_max_pos <= 0 || !positive(c->low_freq_factor) || !positive(c->high_freq_factor) ||
+       c->high_freq_factor <= c->low_freq_factor))
+    return false;
+  for (int i = 0; i < n; ++i) {
+    double w = std::pow(base, -2.0 * i / R);
+    double keep = 1.0;  // share of the unscaled frequency
+    switch (c->scaling) {
+      case KV4_ROPE_SCALE_NONE:
+      case KV4_ROPE_SCALE_NTK: break;
+      case KV4_ROPE_SCALE_LINEAR: keep = 0.0; break;
+      case KV4_ROPE_SCALE_YARN: keep = 1.0 - std::fmin(std::fmax((i - low) / (high - low), 0.0), 1.0); break;
+      case KV4_ROPE_SCALE_BANDS:
+        keep = std::fmin(std::fmax((L * w / kTwoPi - c->low_freq_factor) / (c->high_freq_factor - c->low_freq_factor), 0.0), 1.0);
+        break;
+      default: return false;
+    }
+    if (keep < 1.0) w = keep * w + (1.0 - keep) * w / f;
+    turns[i] = w / kTwoPi;
+  }
+  return true;
+}
+
+kv4_status kv4_rope_table(const kv4_rope_config* cfg, float* table, void* stream) {
+  if (!cfg || !table || !aligned(table, 16) || cfg->max_pos <= 0 || cfg->rotary_dim <= 0) return KV4_ERR_INVALID_ARG;
+  if (cfg->rotary_dim % 8 || cfg->rotary_dim > 128) return KV4_ERR_UNSUPPORTED;
+  kv4::RopeTableArgs a{};
+  if (!rope_frequencies(cfg, a.turns, &a.mult)) return KV4_ERR_INVALID_ARG;
+  a.table = reinterpret_cast<float2*>(table);
+  a.max_pos = cfg->max_pos;
+  a.R = cfg->rotary_dim;
+  return kv4::launch_rope_table(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KV4_OK : KV4_ERR_CUDA;
+}
+
+kv4_status kv4_rope(const kv4_rope_params* rope, int T, int Hq, int Hkv, int D, const void* q, kv4_dtype q_dtype,
+                    int64_t q_stride, const void* k, kv4_dtype k_dtype, int64_t k_stride, const int32_t* pos, void* q_out,
+                    kv4_dtype q_out_dtype, int64_t q_out_stride, void* k_out, kv4_dtype k_out_dtype, int64_t k_out_stride,
+                    void* stream) {
+  if (T < 0 || Hq < 0 || Hkv < 0) return KV4_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return KV4_ERR_UNSUPPORTED;
+  const kv4_status st = check_rope(rope, D);
+  if (st != KV4_OK) return st;
+  if (T == 0 || Hq + Hkv == 0) return KV4_OK;
+  if (!pos) return KV4_ERR_INVALID_ARG;
+  if (Hq > (1 << 20) || Hkv > (1 << 20) || static_cast<long long>(T) * (Hq + Hkv) > kMaxVectors) return KV4_ERR_UNSUPPORTED;
+  const int64_t qr = static_cast<int64_t>(Hq) * D, kr = static_cast<int64_t>(Hkv) * D;
+  if (Hq && (!rows_ok(q, q_dtype, q_stride, qr) || !rows_ok(q_out, q_out_dtype, q_out_stride, qr))) return KV4_ERR_INVALID_ARG;
+  if (Hkv && (!rows_ok(k, k_dtype, k_stride, kr) || !rows_ok(k_out, k_out_dtype, k_out_stride, kr))) return KV4_ERR_INVALID_ARG;
+  if (Hq && q == q_out && (q_dtype != q_out_dtype || q_stride != q_out_stride)) return KV4_ERR_INVALID_ARG;
+  if (Hkv && k == k_out && (k_dtype != k_out_dtype || k_stride != k_out_stride)) return KV4_ERR_INVALID_ARG;
+  uint32_t* err = nullptr;
+  if (!device_info(&err, nullptr)) return KV4_ERR_CUDA;
+  kv4::RopeArgs a = rope_args(rope, err);
+  a.q = q;
+  a.q_dtype = q_dtype;
+  a.q_stride = q_stride;
+  a.k = k;
+  a.k_dtype = k_dtype;
+  a.k_stride = k_stride;
+  a.q_out = q_out;
+  a.q_out_dtype = q_out_dtype;
+  a.q_out_stride = q_out_stride;
+  a.k_out = k_out;
+  a.k_out_dtype = k_out_dtype;
+  a.k_out_stride = k_out_stride;
+  a.pos = pos;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  return kv4::launch_rope(a, D, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KV4_OK : KV4_ERR_CUDA;
+}
+
+kv4_status kv4_append_rope(kv4_cache* cache, int layer, int T, const kv4_rope_params* rope, const void* q,
+                           kv4_dtype q_dtype, int64_t q_stride, const void* K, kv4_dtype k_dtype, int64_t k_stride,
+                           const void* V, kv4_dtype v_dtype, int64_t v_stride, const int32_t* seq_slot, const int32_t* pos,
+                           const int32_t* lens_after, const int32_t* page_table, int stride, void* q_out,
+                           kv4_dtype q_out_dtype, int64_t q_out_stride, void* stream) {
+  if (!cache || layer < 0 || layer >= cache->cfg.num_layers || T < 0 || stride <= 0) return KV4_ERR_INVALID_ARG;
+  const int D = cache->cfg.head_dim, Hq = q ? cache->cfg.num_q_heads : 0, Hkv = cache->cfg.num_kv_heads;
+  const kv4_status st = check_rope(rope, D);
+  if (st != KV4_OK) return st;
+  if (T == 0) return KV4_OK;
+  if (!seq_slot || !pos || !page_table || (cache->format == FMT_INT4 && !lens_after)) return KV4_ERR_INVALID_ARG;
+  if (cache->format == FMT_MIXED && !cache->allocated[layer]) return KV4_ERR_NO_ALLOCATION;
+  const int64_t qr = static_cast<int64_t>(Hq) * D, kr = static_cast<int64_t>(Hkv) * D;
+  if (!rows_ok(K, k_dtype, k_stride, kr) || !rows_ok(V, v_dtype, v_stride, kr)) return KV4_ERR_INVALID_ARG;
+  if (q && (!rows_ok(q, q_dtype, q_stride, qr) || !rows_ok(q_out, q_out_dtype, q_out_stride, qr))) return KV4_ERR_INVALID_ARG;
+  if (q && q == q_out && (q_dtype != q_out_dtype || q_stride != q_out_stride)) return KV4_ERR_INVALID_ARG;
+  if (static_cast<long long>(T) * (Hq + 2LL * Hkv) > kMaxVectors) return KV4_ERR_UNSUPPORTED;
+  uint32_t* err = nullptr;
+  if (!device_info(&err, nullptr)) return KV4_ERR_CUDA;
+  const kv4::AppendArgs a = cache_args(cache, layer, T, seq_slot, pos, lens_after, page_table, stride, err);
+  kv4::RopeArgs r = rope_args(rope, err);
+  r.q = q;
+  r.q_dtype = q_dtype;
+  r.q_stride = q_stride;
+  r.k = K;
+  r.k_dtype = k_dtype;
+  r.k_stride = k_stride;
+  r.v = V;
+  r.v_dtype = v_dtype;
+  r.v_stride = v_stride;
+  r.q_out = q_out;
+  r.q_out_dtype = q_out_dtype;
+  r.q_out_stride = q_out_stride;
+  r.T = T;
+  r.Hq = Hq;
+  r.Hkv = Hkv;
+  const cudaError_t e = kv4::launch_append_rope(r, a, D, cache->format == FMT_BF16, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KV4_OK : KV4_ERR_CUDA;
+}
+
+kv4_status kv4_gather(kv4_cache* cache, int layer, int T, const int32_t* seq_slot, const int32_t* pos, const int32_t* lens,
+                      const int32_t* page_table, int stride, void* K_out, void* V_out, kv4_dtype out_dtype, void* stream) {
+  if (!cache || layer < 0 || layer >= cache->cfg.num_layers || T < 0 || stride <= 0 || dtype_ok_q(out_dtype) != KV4_OK)
+    return KV4_ERR_INVALID_ARG;
+  if (T == 0 || (!K_out && !V_out)) return KV4_OK;
+  if (!seq_slot || !pos || !page_table || !aligned(K_out, 16) || !aligned(V_out, 16)) return KV4_ERR_INVALID_ARG;
+  if (cache->format == FMT_MIXED && !cache->allocated[layer]) return KV4_ERR_NO_ALLOCATION;
+  if (static_cast<long long>(T) * cache->cfg.num_kv_heads > kMaxVectors) return KV4_ERR_UNSUPPORTED;
+  uint32_t* err = nullptr;
+  if (!device_info(&err, nullptr)) return KV4_ERR_CUDA;
+  const kv4::AppendArgs a = cache_args(cache, layer, T, seq_slot, pos, lens, page_table, stride, err);
+  const cudaError_t e = kv4::launch_gather(a, cache->cfg.head_dim, cache->format == FMT_BF16, K_out, V_out, out_dtype,
+                                           static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KV4_OK : KV4_ERR_CUDA;
 }
 
 kv4_status kv4_get_device_error(uint32_t* bits) {

@@ -37,6 +37,33 @@ struct AppendArgs {
 // followed by D/2 uint8 widths, padded to 16 bytes; the records of all layers follow the pages.
 __host__ __device__ inline size_t mixed_alloc_record_bytes(int D) { return (static_cast<size_t>(D) / 2 * 5 + 15) & ~static_cast<size_t>(15); }
 
+// Rotary positions: the table, and the norm and rotation of q and k head vectors.
+struct RopeTableArgs {
+  float2* table;          // [max_pos][R / 2] (cos, sin)
+  long long max_pos;
+  int R;
+  double mult;            // factor on cos and sin
+  double turns[64];       // turns per position of pair i: frequency / 2 pi
+};
+
+struct RopeArgs {
+  const float* table;     // [max_pos][R / 2][2]
+  int max_pos, R, layout;
+  const void* qw;         // norm weights [D], NULL: no norm
+  const void* kw;
+  int w_dtype;
+  double eps;
+  const void *q, *k, *v;  // [T][heads][D], token strides in elements
+  int q_dtype, k_dtype, v_dtype;
+  long long q_stride, k_stride, v_stride;
+  void *q_out, *k_out;
+  int q_out_dtype, k_out_dtype;
+  long long q_out_stride, k_out_stride;
+  const int32_t* pos;     // kv4_rope only
+  int T, Hq, Hkv;
+  uint32_t* err;
+};
+
 struct ScoreArgs {
   const void* K;          // [T][Hkv][D] keys to score
   int k_dtype;
@@ -94,6 +121,13 @@ int mixed_decode_warps_per_cta();
 int mixed_decode_ctas_per_sm(int D, int G, int value_bits, int key_bits);
 // row_copies: padded key rows by one bulk copy per row instead of the tensor copy (a test hook)
 cudaError_t launch_decode_mixed(DecodeArgs a, int D, int G, int ctas, cudaStream_t st, bool row_copies);
+
+// Rotary positions (kv4_rope.cu).  The append and the read-back serve every cache format: a.alloc
+// set: mixed bit-width keys, a.vbf: bf16 values, bf16_pool: the BF16 pool, else INT4.
+cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t st);
+cudaError_t launch_rope(const RopeArgs& a, int D, cudaStream_t st);
+cudaError_t launch_append_rope(const RopeArgs& q, const AppendArgs& a, int D, bool bf16_pool, cudaStream_t st);
+cudaError_t launch_gather(const AppendArgs& a, int D, bool bf16_pool, void* k_out, void* v_out, int dtype, cudaStream_t st);
 
 // Counts every kernel launch the library issues.
 void note_launches(int n);

@@ -31,7 +31,8 @@ SYMBOLS = (
     "kv4_set_rotation_signs", "kv4_set_value_rotation", "kv4_bf16_query_sizes", "kv4_bf16_cache_init",
     "kv4_bf16_append", "kv4_bf16_decode_workspace_bytes", "kv4_bf16_decode_attn", "kv4_get_device_error",
     "kv4_launch_count", "kv4_status_string", "kv4_version", "kv4_allocate_key_bits", "kv4_set_key_allocation",
-    "kv4_get_key_allocation", "kv4_debug_mixed_row_copies",
+    "kv4_get_key_allocation", "kv4_debug_mixed_row_copies", "kv4_rope_table", "kv4_rope", "kv4_append_rope",
+    "kv4_gather",
 )
 
 
@@ -50,12 +51,30 @@ class kv4_config(ctypes.Structure):
         "recent_window", "hadamard_block", "max_seqs", "max_pages", "value_format", "key_bits", "value_bits")]
 
 
+KV4_ROPE_HALF, KV4_ROPE_INTERLEAVED = 0, 1
+(KV4_ROPE_SCALE_NONE, KV4_ROPE_SCALE_LINEAR, KV4_ROPE_SCALE_NTK, KV4_ROPE_SCALE_YARN,
+ KV4_ROPE_SCALE_BANDS) = range(5)
+
+
+class kv4_rope_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("rotary_dim", "max_pos", "scaling", "original_max_pos")] + [
+        (n, ctypes.c_double) for n in ("base", "factor", "low_freq_factor", "high_freq_factor", "beta_fast",
+                                       "beta_slow", "attention_factor")]
+
+
+class kv4_rope_params(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("max_pos", ctypes.c_int), ("rotary_dim", ctypes.c_int),
+                ("layout", ctypes.c_int), ("weight_dtype", ctypes.c_int), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing; build it with `python -m int4_kv_cache_append_b200.build`")
     L = ctypes.CDLL(LIB_PATH)
     P, I, S, U = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64
     cfgp = ctypes.POINTER(kv4_config)
+    LL, ropep = ctypes.c_int64, ctypes.POINTER(kv4_rope_params)
     i32p = ctypes.c_void_p
     sig = {
         "kv4_query_sizes": (I, [cfgp, ctypes.POINTER(S), ctypes.POINTER(S)]),
@@ -82,6 +101,10 @@ def _load():
         "kv4_allocate_key_bits": (I, [P, I, I, P, I, P]),
         "kv4_set_key_allocation": (I, [P, I, P, P, P]),
         "kv4_get_key_allocation": (I, [P, I, P, P, P]),
+        "kv4_rope_table": (I, [ctypes.POINTER(kv4_rope_config), P, P]),
+        "kv4_rope": (I, [ropep, I, I, I, I, P, I, LL, P, I, LL, i32p, P, I, LL, P, I, LL, P]),
+        "kv4_append_rope": (I, [P, I, I, ropep, P, I, LL, P, I, LL, P, I, LL, i32p, i32p, i32p, i32p, I, P, I, LL, P]),
+        "kv4_gather": (I, [P, I, I, i32p, i32p, i32p, i32p, I, P, P, I, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -114,6 +137,35 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+def _rows(t, what: str):
+    """(pointer, kv4_dtype, elements between tokens) of a [T][heads][D] tensor whose heads are
+    contiguous in a token; (None, 0, 0) for None."""
+    if t is None:
+        return None, 0, 0
+    if not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{what}: device tensor [T][heads][D] expected")
+    T, H, D = t.shape
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{what}: float32, bfloat16 or float16 expected, got {t.dtype}")
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{what}: the heads of a token must be contiguous")
+    return t.data_ptr(), _DTYPES[t.dtype], (t.stride(0) if T > 1 else H * D)
+
+
+def _i32(t, what: str):
+    if t is not None and t.dtype != torch.int32:
+        raise ValueError(f"{what}: int32 tensor expected, got {t.dtype}")
+    return _ptr(t)
+
+
+def _on_current_device(*tensors) -> None:
+    """The library launches on the current device."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
 def _stream(stream) -> int | None:
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
@@ -122,8 +174,11 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
+_DTYPES = {torch.float32: KV4_F32, torch.bfloat16: KV4_BF16, torch.float16: KV4_F16}
+
+
 def dtype_code(t: torch.Tensor) -> int:
-    return {torch.float32: KV4_F32, torch.bfloat16: KV4_BF16, torch.float16: KV4_F16}[t.dtype]
+    return _DTYPES[t.dtype]
 
 
 # ------------------------------------------------------------------------ C entry points
@@ -235,6 +290,54 @@ def kv4_get_key_allocation(handle, layer, Hkv, D, stream=None):
     return w, sg
 
 
+def kv4_rope_table(cfg: kv4_rope_config, table, stream=None):
+    """Write the cos/sin table fp32 [max_pos][rotary_dim / 2][2] of a rotary configuration."""
+    _check("kv4_rope_table", lib.kv4_rope_table(ctypes.byref(cfg), _ptr(table), _stream(stream)))
+
+
+def kv4_rope(params: kv4_rope_params, q, k, pos, q_out, k_out, stream=None):
+    """Norm and rotate T tokens' queries [T][Hq][D] and keys [T][Hkv][D] (either may be None)."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k expected")
+    for src, dst, what in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+        if (src is None) != (dst is None) or (src is not None and src.shape != dst.shape):
+            raise ValueError(f"{what}: the shape of its input expected")
+    if q is not None and k is not None and (q.shape[0], q.shape[2]) != (k.shape[0], k.shape[2]):
+        raise ValueError("q and k differ in tokens or head size")
+    T, D = int(x.shape[0]), int(x.shape[2])
+    if pos.numel() != T:
+        raise ValueError("pos: one position per token expected")
+    _on_current_device(q, k, pos, q_out, k_out)
+    _check("kv4_rope", lib.kv4_rope(ctypes.byref(params), T, q.shape[1] if q is not None else 0,
+                                    k.shape[1] if k is not None else 0, D, *_rows(q, "q"), *_rows(k, "k"),
+                                    _i32(pos, "pos"), *_rows(q_out, "q_out"), *_rows(k_out, "k_out"), _stream(stream)))
+
+
+def kv4_append_rope(handle, layer, params: kv4_rope_params, q, K, V, seq_slot, pos, lens_after, page_table, stride,
+                    q_out, stream=None):
+    """Append keys and values [T][Hkv][D], the keys normed and rotated on the way; q_out receives the
+    normed and rotated queries (q and q_out None: append only)."""
+    if (q is None) != (q_out is None) or (q is not None and q.shape != q_out.shape):
+        raise ValueError("q_out: the shape of q expected")
+    T = int(seq_slot.numel())
+    if pos.numel() != T or any(x is not None and x.shape[0] != T for x in (q, K, V)) or K.shape != V.shape:
+        raise ValueError("q, K, V, seq_slot and pos must have the same tokens")
+    _on_current_device(q, K, V, seq_slot, pos, lens_after, page_table, q_out)
+    _check("kv4_append_rope", lib.kv4_append_rope(handle, layer, T, ctypes.byref(params), *_rows(q, "q"), *_rows(K, "K"),
+                                                  *_rows(V, "V"), _i32(seq_slot, "seq_slot"), _i32(pos, "pos"),
+                                                  _i32(lens_after, "lens_after"), _i32(page_table, "page_table"), stride,
+                                                  *_rows(q_out, "q_out"), _stream(stream)))
+
+
+def kv4_gather(handle, layer, T, seq_slot, pos, lens, page_table, stride, K_out, V_out, out_dtype, stream=None):
+    """Read T cached positions back as dense keys and values [T][Hkv][D] in their original basis."""
+    _on_current_device(seq_slot, pos, lens, page_table, K_out, V_out)
+    _check("kv4_gather", lib.kv4_gather(handle, layer, T, _i32(seq_slot, "seq_slot"), _i32(pos, "pos"), _i32(lens, "lens"),
+                                        _i32(page_table, "page_table"), stride, _ptr(K_out), _ptr(V_out), out_dtype,
+                                        _stream(stream)))
+
+
 def kv4_bf16_query_sizes(cfg: kv4_config) -> int:
     pool = ctypes.c_size_t()
     _check("kv4_bf16_query_sizes", lib.kv4_bf16_query_sizes(ctypes.byref(cfg), ctypes.byref(pool)))
@@ -310,7 +413,101 @@ class Geometry:
         return H * P * (D // 2 + 4 + 2 * D if self.value_format == KV4_VALUES_BF16 else D + 8)
 
 
-class Cache:
+@dataclass
+class RopeGeometry:
+    rotary_dim: int
+    max_pos: int
+    layout: int = KV4_ROPE_HALF
+    base: float = 10000.0
+    scaling: int = KV4_ROPE_SCALE_NONE
+    factor: float = 1.0
+    original_max_pos: int = 0
+    low_freq_factor: float = 1.0
+    high_freq_factor: float = 4.0
+    beta_fast: float = 32.0
+    beta_slow: float = 1.0
+    attention_factor: float = 0.0
+
+    def c(self) -> kv4_rope_config:
+        return kv4_rope_config(self.rotary_dim, self.max_pos, self.scaling, self.original_max_pos, self.base, self.factor,
+                               self.low_freq_factor, self.high_freq_factor, self.beta_fast, self.beta_slow,
+                               self.attention_factor)
+
+
+class Rope:
+    """A rotary embedding with its torch-allocated table and the per-head norm weights (None: no
+    norm); the weights are [head_dim] tensors of one type that the caller keeps."""
+
+    def __init__(self, geo: RopeGeometry, q_weight=None, k_weight=None, eps: float = 1e-6, device="cuda", stream=None):
+        for w in (q_weight, k_weight):
+            if w is not None and (w.dim() != 1 or not w.is_contiguous() or w.dtype not in _DTYPES):
+                raise ValueError("norm weights: contiguous [head_dim] tensors expected")
+        if q_weight is not None and k_weight is not None and (q_weight.dtype, q_weight.shape) != (k_weight.dtype, k_weight.shape):
+            raise ValueError("norm weights: one type and size expected")
+        self.geo, self.q_weight, self.k_weight, self.eps = geo, q_weight, k_weight, eps
+        self.cfg = geo.c()
+        self.table = torch.empty((max(geo.max_pos, 0), max(geo.rotary_dim, 0) // 2, 2), dtype=torch.float32, device=device)
+        self.build(stream)
+        w = q_weight if q_weight is not None else k_weight
+        self.params = kv4_rope_params(self.table.data_ptr(), geo.max_pos, geo.rotary_dim, geo.layout,
+                                      dtype_code(w) if w is not None else KV4_F32, _ptr(q_weight), _ptr(k_weight), eps)
+
+    def build(self, stream=None) -> torch.Tensor:
+        """(Re)write the table on the stream; other streams must wait for it."""
+        _on_current_device(self.table)
+        kv4_rope_table(self.cfg, self.table, stream)
+        return self.table
+
+    def check_head_dim(self, D: int) -> None:
+        for w in (self.q_weight, self.k_weight):
+            if w is not None and w.numel() != D:
+                raise ValueError(f"norm weights of {w.numel()} elements for heads of {D}")
+
+    def apply(self, q, k, pos, q_out=None, k_out=None, stream=None):
+        """Normed and rotated (q, k); new tensors of the inputs' types unless outputs are given."""
+        for x in (q, k):
+            if x is not None:
+                self.check_head_dim(int(x.shape[-1]))
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        kv4_rope(self.params, q, k, pos, q_out, k_out, stream)
+        return q_out, k_out
+
+
+class _RopeCacheMixin:
+    """kv4_append_rope and kv4_gather of a cache object (both kinds of handle)."""
+
+    def append_rope(self, layer, rope: Rope, q, K, V, seq_slot, pos, lens_after, page_table, q_out=None, stream=None):
+        """Append K and V [T][Hkv][D], the keys normed and rotated; returns the normed and rotated
+        queries (None when q is None).  lens_after is not read by a BF16 or mixed-key cache."""
+        g = self.geo
+        rope.check_head_dim(g.head_dim)
+        if tuple(K.shape[1:]) != (g.num_kv_heads, g.head_dim) or (q is not None and tuple(q.shape[1:]) != (g.num_q_heads, g.head_dim)):
+            raise ValueError("q [T][Hq][D] and K, V [T][Hkv][D] of the cache's geometry expected")
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        kv4_append_rope(self.handle, layer, rope.params, q, K, V, seq_slot, pos, lens_after, page_table,
+                        int(page_table.shape[1]), q_out, stream)
+        return q_out
+
+    def gather(self, layer, seq_slot, pos, page_table, lens=None, dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
+        """Cached positions as dense (K, V) [T][Hkv][D] in their original basis."""
+        T = int(seq_slot.numel())
+        if pos.numel() != T:
+            raise ValueError("one position per seq_slot expected")
+        shape = (T, self.geo.num_kv_heads, self.geo.head_dim)
+        k_out = torch.empty(shape, dtype=dtype, device=pos.device) if k_out is None else k_out
+        v_out = torch.empty(shape, dtype=dtype, device=pos.device) if v_out is None else v_out
+        if tuple(k_out.shape) != shape or tuple(v_out.shape) != shape or k_out.dtype != v_out.dtype:
+            raise ValueError("k_out and v_out [T][Hkv][D] of one type expected")
+        kv4_gather(self.handle, layer, T, seq_slot, pos, lens, page_table, int(page_table.shape[1]), k_out, v_out,
+                   dtype_code(k_out), stream)
+        return k_out, v_out
+
+
+class Cache(_RopeCacheMixin):
     """INT4 cache with torch-allocated page pool and side cache (uint8 tensors)."""
 
     def __init__(self, geo: Geometry, device="cuda", fill: int | None = None):
@@ -369,7 +566,7 @@ class Cache:
             pass
 
 
-class BF16Cache:
+class BF16Cache(_RopeCacheMixin):
     """BF16-KV baseline cache (same page table conventions, bf16 K and V in the pages)."""
 
     def __init__(self, geo: Geometry, device="cuda"):
