@@ -77,6 +77,9 @@ typedef enum { KV4_F32 = 0, KV4_BF16 = 1, KV4_F16 = 2 } kv4_dtype;
                                        workspace (left by a decode that stopped early) and
                                        skipped it                                               */
 
+#define KV4_DEVERR_GROUP 0x20u      /* group_start is not non-decreasing within [0, B]: the call shared
+                                       nothing and every sequence read its own pages            */
+
 /* Storage formats (kv4_config.value_format). */
 #define KV4_VALUES_INT4 0  /* values as per-token affine INT4 (INT8 in the side cache): KV4       */
 #define KV4_VALUES_BF16 1  /* values kept in bf16 in the pages and the side cache, keys as in KV4 */
@@ -303,6 +306,31 @@ kv4_status kv4_bf16_decode_attn(kv4_cache* cache, int layer, int B, const void* 
                                 const int32_t* page_table, int stride, const int32_t* lens,
                                 int max_len_hint, float* out, float* lse, void* workspace,
                                 size_t ws_bytes, void* stream);
+
+/*
+ * kv4_decode_attn_shared: kv4_decode_attn for a batch whose sequences share long prefixes, as the
+ * answers sampled for one prompt do: each group's prefix is read and decoded once for all of its
+ * sequences.  Rows [group_start[i], group_start[i + 1]) of the batch form group i (device int32
+ * [n_groups + 1], non-decreasing, within [0, B]; rows before the first and after the last group
+ * share nothing), and the first prefix_len[i] positions (device int32 [n_groups]) of its sequences
+ * lie in pages with the same contents; they are read through the page-table row of the group's
+ * first sequence, whole 16 positions at a time (what is left of prefix_len past a multiple of 16
+ * is read as each sequence's own).  The page ids of the other rows may be the same (pages shared)
+ * or not (copies).  A prefix may be longer than some of its sequences; each attends what it would
+ * in kv4_decode_attn: its own INT8 sink and recent rows, and the INT4 positions before its recent
+ * window.  Attention of the INT4 cache with INT4 values (KV4_ERR_UNSUPPORTED for KV4_VALUES_BF16,
+ * KV4_ERR_INVALID_ARG for the other handles), signs and value rotation included.
+ *   out          device [B][Hq][D] of out_dtype, 16-byte aligned; lse fp32 [B][Hq] or NULL
+ *   workspace    kv4_decode_shared_workspace_bytes(B, n_groups) bytes, as for kv4_decode_attn
+ * Precision: within the prefix the rotated query and the probabilities enter the products as fp16
+ * (11 bits), keys as exact codes and values as fp16; statistics and sums are fp32.  The other
+ * arguments are those of kv4_decode_attn.  Three launches: prefix, own positions, merge.
+ */
+kv4_status kv4_decode_shared_workspace_bytes(const kv4_cache* cache, int B, int n_groups, size_t* bytes);
+kv4_status kv4_decode_attn_shared(kv4_cache* cache, int layer, int B, const void* q, kv4_dtype q_dtype,
+                                  const int32_t* page_table, int stride, const int32_t* lens, int n_groups,
+                                  const int32_t* group_start, const int32_t* prefix_len, int max_len_hint, void* out,
+                                  kv4_dtype out_dtype, float* lse, void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * Rotary positions up to the cache.  Between a model's query/key/value projection and the decode lie

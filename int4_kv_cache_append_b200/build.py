@@ -23,7 +23,7 @@ COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-ftz=fal
           "-Xptxas", "-v"]
 
 LIBS = {
-    "libkv4.so": ["kv4_api.cu", "kv4_append.cu", "kv4_decode.cu", "kv4_bf16.cu", "kv4_mixed.cu", "kv4_rope.cu"],
+    "libkv4.so": ["kv4_api.cu", "kv4_append.cu", "kv4_decode.cu", "kv4_bf16.cu", "kv4_mixed.cu", "kv4_rope.cu", "kv4_shared.cu"],
     "libkv4gen.so": ["kv4gen.cu"],
 }
 

@@ -253,9 +253,27 @@ kv4::RopeArgs rope_args(const kv4_rope_params* r, uint32_t* err) {
 // Warps of the rotary kernels are counted in 32 bits.
 constexpr long long kMaxVectors = 1LL << 26;
 
+// What kv4_decode_attn_shared adds.
+struct SharedPrefix {
+  int n_groups;
+  const int32_t* group_start;
+  const int32_t* prefix_len;
+  int out_dtype;
+};
+
+// Its workspace after the decode's own: the prefix records, the own-tile list, the prefix partials.
+size_t shared_rows_bytes(const kv4_cache* c, int B) {
+  return static_cast<size_t>(B) * c->cfg.num_kv_heads * 16 + align16(static_cast<size_t>(B) * 4);
+}
+size_t shared_part_bytes(const kv4_cache* c, int B, int n_groups, int sms) {
+  const size_t G = static_cast<size_t>(c->cfg.num_q_heads / c->cfg.num_kv_heads), rb = static_cast<size_t>(kv4::shared_row_block());
+  const size_t segs = static_cast<size_t>(c->cfg.num_kv_heads) * (static_cast<size_t>(n_groups) + static_cast<size_t>(B) * G / rb);
+  return (static_cast<size_t>(sms) + segs) * rb * (static_cast<size_t>(c->cfg.head_dim) + 4) * sizeof(float);
+}
+
 kv4_status decode_common(kv4_cache* c, int fmt, int layer, int B, const void* q, kv4_dtype qd,
                          const int32_t* page_table, int stride, const int32_t* lens, int max_len_hint, float* out,
-                         float* lse, void* ws, size_t ws_bytes, void* stream) {
+                         float* lse, void* ws, size_t ws_bytes, void* stream, const SharedPrefix* sp = nullptr) {
   if (!c || c->format != fmt) return KV4_ERR_INVALID_ARG;
   if (layer < 0 || layer >= c->cfg.num_layers || B < 0 || B > c->cfg.max_seqs || stride <= 0 || max_len_hint < 0)
     return KV4_ERR_INVALID_ARG;
@@ -279,13 +297,16 @@ kv4_status decode_common(kv4_cache* c, int fmt, int layer, int B, const void* q,
     if (want < 1) want = 1;
     if (want < ctas) ctas = static_cast<int>(want);
   }
-  if (ws_bytes < workspace_for(c, B, ctas)) return KV4_ERR_WORKSPACE;
+  const size_t own_ws = workspace_for(c, B, ctas);
+  if (ws_bytes < own_ws + (sp ? shared_rows_bytes(c, B) + shared_part_bytes(c, B, sp->n_groups, sms) : 0)) return KV4_ERR_WORKSPACE;
   {
     // work units are counted in 32 bits on the device: bound the worst case (every sequence at
     // the page-table capacity)
     const long long tiles = (static_cast<long long>(stride) * c->cfg.page_size + 15) / 16;
     const long long units = static_cast<long long>(B) * c->cfg.num_kv_heads * (tiles + 2LL * c->nt8);
     if (units >= (1LL << 31)) return KV4_ERR_UNSUPPORTED;
+    // so are the prefix kernel's: every segment at the page-table capacity
+    if (sp && (sp->n_groups + static_cast<long long>(B)) * c->cfg.num_kv_heads * (tiles / 8 + 2) >= (1LL << 31)) return KV4_ERR_UNSUPPORTED;
   }
   kv4::DecodeArgs a{};
   a.pool = c->pool + static_cast<size_t>(layer) * c->pool_layer_bytes;
@@ -329,6 +350,19 @@ kv4_status decode_common(kv4_cache* c, int fmt, int layer, int B, const void* q,
   }
   const int G = c->cfg.num_q_heads / c->cfg.num_kv_heads;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (sp) {
+    uint8_t* rows = static_cast<uint8_t*>(ws) + own_ws;
+    a.n_groups = sp->n_groups;
+    a.group_start = sp->group_start;
+    a.prefix_len = sp->prefix_len;
+    a.out_dtype = sp->out_dtype;
+    a.PW = sms;
+    a.early = 0;  // its first kernel writes what the decode's schedule reads
+    a.pmeta = reinterpret_cast<uint4*>(rows);
+    a.own = reinterpret_cast<int*>(rows + static_cast<size_t>(B) * c->cfg.num_kv_heads * 16);
+    a.ppart = reinterpret_cast<float*>(rows + shared_rows_bytes(c, B));
+    return kv4::launch_decode_shared(a, c->cfg.head_dim, G, ctas, st) == cudaSuccess ? KV4_OK : KV4_ERR_CUDA;
+  }
   const cudaError_t e = fmt == FMT_INT4    ? kv4::launch_decode_int4(a, c->cfg.head_dim, G, ctas, st)
                         : fmt == FMT_MIXED ? kv4::launch_decode_mixed(a, c->cfg.head_dim, G, ctas, st, c->mixed_rows != 0)
                                            : kv4::launch_decode_bf16(a, c->cfg.head_dim, G, ctas, st);
@@ -403,6 +437,28 @@ kv4_status kv4_decode_attn(kv4_cache* cache, int layer, int B, const void* q, kv
                            float* lse, void* workspace, size_t ws_bytes, void* stream) {
   return decode_common(cache, own_format(cache), layer, B, q, q_dtype, page_table, stride, lens, max_len_hint, out,
                        lse, workspace, ws_bytes, stream);
+}
+
+kv4_status kv4_decode_shared_workspace_bytes(const kv4_cache* cache, int B, int n_groups, size_t* bytes) {
+  if (!cache || cache->format != FMT_INT4 || B < 0 || n_groups < 0 || !bytes) return KV4_ERR_INVALID_ARG;
+  if (cache->cfg.value_format != KV4_VALUES_INT4) return KV4_ERR_UNSUPPORTED;
+  int sms = 0;
+  if (!device_info(nullptr, &sms)) return KV4_ERR_CUDA;
+  *bytes = workspace_for(cache, B, decode_ctas_full(cache, sms)) + shared_rows_bytes(cache, B) + shared_part_bytes(cache, B, n_groups, sms);
+  return KV4_OK;
+}
+
+kv4_status kv4_decode_attn_shared(kv4_cache* cache, int layer, int B, const void* q, kv4_dtype q_dtype,
+                                  const int32_t* page_table, int stride, const int32_t* lens, int n_groups,
+                                  const int32_t* group_start, const int32_t* prefix_len, int max_len_hint, void* out,
+                                  kv4_dtype out_dtype, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  if (!cache || cache->format != FMT_INT4 || n_groups < 0 || n_groups > (1 << 20) || dtype_ok_q(out_dtype) != KV4_OK)
+    return KV4_ERR_INVALID_ARG;
+  if (cache->cfg.value_format != KV4_VALUES_INT4) return KV4_ERR_UNSUPPORTED;
+  if (B > 0 && n_groups > 0 && (!group_start || !prefix_len)) return KV4_ERR_INVALID_ARG;
+  const SharedPrefix sp{n_groups, group_start, prefix_len, out_dtype};
+  return decode_common(cache, FMT_INT4, layer, B, q, q_dtype, page_table, stride, lens, max_len_hint, static_cast<float*>(out),
+                       lse, workspace, ws_bytes, stream, &sp);
 }
 
 // No-allocation decode: the split-K partials go to this file-scope device array instead of a

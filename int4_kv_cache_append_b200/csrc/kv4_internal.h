@@ -99,6 +99,15 @@ struct DecodeArgs {
   const uint8_t* alloc;   // this layer's block allocation records
   int kbits, vbits;       // key bits per dimension (average), value bits per dimension
   uint32_t* err;
+  // kv4_decode_attn_shared
+  int n_groups;
+  const int32_t* group_start;  // [n_groups + 1] rows of the groups
+  const int32_t* prefix_len;   // [n_groups]
+  int* own;               // [B] first own 16-position tile of each sequence (written by the prefix kernel)
+  uint4* pmeta;           // [B][Hkv] prefix partials: first index, count, row of head 0 (written likewise)
+  float* ppart;           // prefix partials [PW + segments][rows][D + 4]
+  int PW;                 // thread blocks of the prefix kernel
+  int out_dtype;          // type of `out` (float elsewhere)
 };
 
 // Launchers return cudaSuccess or the launch error.  `grid_ctas` is filled with the CTA count
@@ -113,6 +122,10 @@ size_t decode_smem_bytes(int D, int G);
 size_t bf16_decode_smem_bytes(int D, int G);
 cudaError_t launch_decode_int4(DecodeArgs a, int D, int G, int ctas, cudaStream_t st);
 cudaError_t launch_decode_bf16(DecodeArgs a, int D, int G, int ctas, cudaStream_t st);
+
+// Shared prefixes (kv4_shared.cu): a.out holds elements of a.out_dtype.
+int shared_row_block();  // query rows of one prefix segment
+cudaError_t launch_decode_shared(DecodeArgs a, int D, int G, int ctas, cudaStream_t st);
 
 // Mixed bit-width key cache (RoPE-block bit allocation): scoring + allocation, append, decode.
 cudaError_t launch_mixed_score(const ScoreArgs& a, int D, cudaStream_t st);

@@ -23,6 +23,7 @@ LIB_PATH = os.path.join(_HERE, "libkv4.so")
  KV4_ERR_NO_ALLOCATION) = range(7)
 KV4_F32, KV4_BF16, KV4_F16 = 0, 1, 2
 KV4_DEVERR_PAGE_RANGE, KV4_DEVERR_WAIT_LIMIT, KV4_DEVERR_LENGTH, KV4_DEVERR_RANGE, KV4_DEVERR_RECORD = 0x1, 0x2, 0x4, 0x8, 0x10
+KV4_DEVERR_GROUP = 0x20
 
 # every entry point declared in include/kv4.h
 SYMBOLS = (
@@ -32,7 +33,7 @@ SYMBOLS = (
     "kv4_bf16_append", "kv4_bf16_decode_workspace_bytes", "kv4_bf16_decode_attn", "kv4_get_device_error",
     "kv4_launch_count", "kv4_status_string", "kv4_version", "kv4_allocate_key_bits", "kv4_set_key_allocation",
     "kv4_get_key_allocation", "kv4_debug_mixed_row_copies", "kv4_rope_table", "kv4_rope", "kv4_append_rope",
-    "kv4_gather",
+    "kv4_gather", "kv4_decode_shared_workspace_bytes", "kv4_decode_attn_shared",
 )
 
 
@@ -104,6 +105,8 @@ def _load():
         "kv4_rope_table": (I, [ctypes.POINTER(kv4_rope_config), P, P]),
         "kv4_rope": (I, [ropep, I, I, I, I, P, I, LL, P, I, LL, i32p, P, I, LL, P, I, LL, P]),
         "kv4_append_rope": (I, [P, I, I, ropep, P, I, LL, P, I, LL, P, I, LL, i32p, i32p, i32p, i32p, I, P, I, LL, P]),
+        "kv4_decode_shared_workspace_bytes": (I, [P, I, I, ctypes.POINTER(S)]),
+        "kv4_decode_attn_shared": (I, [P, I, I, P, I, i32p, I, i32p, I, i32p, i32p, I, P, I, P, P, S, P]),
         "kv4_gather": (I, [P, I, I, i32p, i32p, i32p, i32p, I, P, P, I, P]),
     }
     for name, (res, args) in sig.items():
@@ -338,6 +341,22 @@ def kv4_gather(handle, layer, T, seq_slot, pos, lens, page_table, stride, K_out,
                                         _stream(stream)))
 
 
+def kv4_decode_shared_workspace_bytes(handle, B, n_groups) -> int:
+    n = ctypes.c_size_t()
+    _check("kv4_decode_shared_workspace_bytes", lib.kv4_decode_shared_workspace_bytes(handle, B, n_groups, ctypes.byref(n)))
+    return n.value
+
+
+def kv4_decode_attn_shared(handle, layer, B, q, q_dtype, page_table, stride, lens, n_groups, group_start, prefix_len,
+                           max_len_hint, out, out_dtype, lse, workspace, ws_bytes, stream=None):
+    """kv4_decode_attn for groups of batch rows that share a prefix, each read once per group."""
+    _on_current_device(q, page_table, lens, group_start, prefix_len, out, lse, workspace)
+    _check("kv4_decode_attn_shared", lib.kv4_decode_attn_shared(
+        handle, layer, B, _ptr(q), q_dtype, _i32(page_table, "page_table"), stride, _i32(lens, "lens"), n_groups,
+        _i32(group_start, "group_start"), _i32(prefix_len, "prefix_len"), max_len_hint, _ptr(out), out_dtype, _ptr(lse),
+        _ptr(workspace), ws_bytes, _stream(stream)))
+
+
 def kv4_bf16_query_sizes(cfg: kv4_config) -> int:
     pool = ctypes.c_size_t()
     _check("kv4_bf16_query_sizes", lib.kv4_bf16_query_sizes(ctypes.byref(cfg), ctypes.byref(pool)))
@@ -521,6 +540,7 @@ class Cache(_RopeCacheMixin):
             self.side.fill_(fill)
         self.handle = kv4_cache_init(self.cfg, self.pool, self.side)
         self._ws = None
+        self._shared_ws = {}
 
     def layer_views(self, layer: int):
         """(pages of the layer, side cache of the layer) as uint8 views."""
@@ -552,6 +572,37 @@ class Cache(_RopeCacheMixin):
         ws = workspace if workspace is not None else self.workspace(B)
         kv4_decode_attn(self.handle, layer, B, q, dtype_code(q), page_table, int(page_table.shape[1]), lens,
                         max_len_hint, out, lse, ws, ws.numel(), stream)
+        return out
+
+    def shared_workspace(self, B: int, n_groups: int) -> torch.Tensor:
+        """The cache's workspace for this batch shape.  It is kept (a captured graph may hold it);
+        calls that overlap on the GPU need workspaces of their own."""
+        ws = self._shared_ws.get((B, n_groups))
+        if ws is None:
+            ws = torch.empty(kv4_decode_shared_workspace_bytes(self.handle, B, n_groups), dtype=torch.uint8,
+                             device=self.pool.device)
+            self._shared_ws[(B, n_groups)] = ws
+        return ws
+
+    def decode_shared(self, layer, q, page_table, lens, group_start, prefix_len, out=None, lse=None, max_len_hint=0,
+                      workspace=None, stream=None):
+        """Decode of a batch whose row groups [group_start[i], group_start[i + 1]) share their first
+        prefix_len[i] positions; out has q's type unless given."""
+        B, n = int(lens.numel()), int(prefix_len.numel())
+        shape = (B, self.geo.num_q_heads, self.geo.head_dim)
+        if tuple(q.shape) != shape or page_table.shape[0] < B:
+            raise ValueError("q [B][Hq][D] and a page-table row per sequence expected")
+        if group_start.numel() != n + 1:
+            raise ValueError("group_start: one entry more than prefix_len expected")
+        if out is None:
+            out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        elif tuple(out.shape) != shape:
+            raise ValueError("out [B][Hq][D] expected")
+        if workspace is None:
+            workspace = self.shared_workspace(B, n)
+        kv4_decode_attn_shared(self.handle, layer, B, q, dtype_code(q), page_table, int(page_table.shape[1]), lens, n,
+                               group_start, prefix_len, max_len_hint, out, dtype_code(out), lse, workspace,
+                               workspace.numel(), stream)
         return out
 
     def close(self):
