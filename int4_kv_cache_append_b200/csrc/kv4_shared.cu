@@ -1,13 +1,32 @@
 // kv4_shared.cu -- kv4_decode_attn_shared: decode attention for batches whose sequences share prefixes.
+//
+// The prefix of a group is one attention of many query rows (sequences x query heads of a KV head)
+// over the same keys, so it runs on the tensor cores: positions are the 128 rows of the MMA, query
+// rows its columns.  Per 128-position unit of one KV head
+//   S^T [position][row]  = codes of K [128][D]  x  Q^T [D][rows]
+//   logit                = s_t S + z_t sum(q)        (scale and zero after the reduction, fp32)
+//   P                    = exp2(logit - m_row)       (fp16)
+//   O^T [dim][row]      += V^T [D][128]         x  P [128][rows]
+// The codes go from the packed page tile straight into TMEM as the A operands: a key code is the
+// fp16 subnormal c 2^-24 (one mask, exact), a value is dequantised to fp16 (z + s c, one rounding).
+// Keeping A in TMEM leaves shared memory to the packed tiles, Q and P; with the positions as the
+// MMA's rows its cost follows the number of query rows, and s_t and z_t are one thread's constants.
+//
+// A thread block is 18 warps: two softmax warpgroups (32 of the 64 columns each, a thread per
+// position), a warpgroup unpacking keys, one unpacking values, a warp of bulk copies and a warp
+// that issues the MMAs; K, V, S and P have two buffers, the packed tiles four.  The running maximum
+// of a row is raised only when a logit exceeds it by more than 8 (P then stays below 2^8, far inside
+// fp16): the first unit of a segment sets it, later ones seldom need the rescaling of O.
 #include "kv4_decode_kernel.cuh"
 #include "kv4_quant.cuh"
+#include "kv4_tcgen05.cuh"
 
 namespace kv4 {
 namespace {
 
-constexpr int kRB = 64;          // query rows of a prefix segment
-constexpr int kTile = 128;       // positions of a prefix unit
-constexpr int kPrefixThreads = 256;
+constexpr int kRB = 64;          // query rows of a prefix segment: the MMA's columns
+constexpr int kTile = 128;       // positions of a prefix unit: the MMA's rows
+constexpr int kRaw = 4;          // buffers of packed tiles
 
 // ------------------------------------------------------------------ the prefix schedule
 //
@@ -100,15 +119,15 @@ __device__ void make_plan(const DecodeArgs& a, int lane, Plan& p) {
   }
 }
 
-// Rows without a prefix partial, and every row's first own tile: spread over the thread blocks.
+// Rows without a prefix partial, and every row's first own tile: spread over the thread blocks, one
+// warp of each.
 template <int G>
-__device__ void write_rows(const DecodeArgs& a, const Plan& p) {
+__device__ void write_rows(const DecodeArgs& a, const Plan& p, int lane) {
   auto plain = [&](int b) {
     a.own[b] = 0;
     for (int g = 0; g < a.Hkv; ++g) a.pmeta[b * a.Hkv + g] = make_uint4(0u, 0u, 0u, 0u);
   };
-  const int tid = threadIdx.x, nt = blockDim.x;
-  const int all = gridDim.x * nt, me = blockIdx.x * nt + tid;
+  const int all = gridDim.x * 32, me = blockIdx.x * 32 + lane;
   if (p.bad || a.n_groups == 0) {
     for (int b = me; b < a.B; b += all) plain(b);
     return;
@@ -119,7 +138,7 @@ __device__ void write_rows(const DecodeArgs& a, const Plan& p) {
   for (int gr = blockIdx.x; gr < a.n_groups; gr += gridDim.x) {
     bool bad;
     const Group g = load_group<G>(a, gr, &bad);
-    for (int i = tid; i < g.n; i += nt) {
+    for (int i = lane; i < g.n; i += 32) {
       if (g.tiles == 0) plain(g.b0 + i);
       else a.own[g.b0 + i] = g.te;
     }
@@ -128,159 +147,634 @@ __device__ void write_rows(const DecodeArgs& a, const Plan& p) {
 
 // ------------------------------------------------------------------ prefix attention
 
+constexpr int kSoftWarps = 8, kKeyWarp0 = 8, kValWarp0 = 12, kCopyWarp = 16, kMmaWarp = 17;
+constexpr int kPrefixThreads = 18 * 32;
+constexpr float kUnset = -1e30f;   // running maximum of a row that has seen no position
+constexpr float kGrow = 8.f;       // a logit this far above the running maximum raises it
+constexpr float kQShift = 64.f;    // queries enter fp16 times this: typical ones are then near one
+
 template <int D>
 struct SmemPrefix {
-  float K[kTile][D + 1];
-  float V[kTile][D];
-  float q[kRB][D];
-  float o[kRB][D];
-  float p[kPrefixThreads / 32][kTile];
-  float m[kRB], l[kRB];
-  int lim[kRB];
+  uint8_t raw[kRaw][8 * Geo<D>::T4B];
+  __half P[2][kRB * kTile];   // [row / 8][position][row % 8]: MN-major core matrices
+  __half Q[kRB * D];          // [k / 8][row][k % 8]: K-major core matrices
+  float4 cst[kRB / 2];        // rows 2j, 2j + 1: sum(q), sum(q), -m, -m
+  float2 mul[kRB / 2];        // rows whose query had to be scaled down to fit fp16: the factor back
+  float alpha[kRB];
+  float red[2][4][32];
+  int lim[kRB];               // end of the row's INT4 positions in the prefix
+  int edge[2];                // smallest and largest lim of the rows
+  int scaled;                 // some row has mul != 1
+  uint32_t ok[kRaw];          // tiles of the buffer that were copied
+  uint64_t raw_full[kRaw], raw_empty[kRaw];
+  uint64_t k_ready[2], v_ready[2], qk_done[2], s_free[2], p_ready[2], pv_done[2];
+  uint64_t q_ready;
+  uint64_t stall;             // never arrived on (kv4_debug_force_wait_timeout)
+  uint32_t tmem;
+  int abort;
   Plan plan;
 };
 
-template <int D, int G, int QT>
-__global__ void __launch_bounds__(kPrefixThreads) prefix_kernel(const DecodeArgs a) {
+// TMEM columns: keys and values as A operands (two fp16 a column), scores, outputs.
+template <int D>
+struct Cols {
+  static constexpr int K = 0, V = 2 * (D / 2), S = V + 2 * (kTile / 2), O = S + 2 * kRB, All = 512;
+  static_assert(O + kRB <= All, "TMEM columns");
+};
+
+// A bounded wait that gives up when any warp of the block has: every role then runs its loop to the
+// end without waiting, so that all of them reach the end of the kernel.
+__device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err, uint64_t limit_ns) {
+  if (mbar_try_wait(bar, parity)) return;
+  if (*abort) return;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1; it < kWaitLimitPolls; ++it) {
+    if (mbar_try_wait(bar, parity)) return;
+    if ((it & 15u) == 0u && (*abort || global_timer_ns() - t0 > limit_ns)) break;
+  }
+  if (!*abort) {
+    *abort = 1;
+    atomicOr(err, KV4_DEVERR_WAIT_LIMIT);
+  }
+}
+
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) arrive(bar);
+}
+
+// One of the two softmax warpgroups in step, with the OR of a predicate.
+__device__ __forceinline__ bool group_or(int id, bool x) {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 q, %1, 0;\n barrier.cta.red.or.pred p, %2, 128, q;\n selp.b32 %0, 1, 0, p;\n}\n"
+               : "=r"(r)
+               : "r"(static_cast<uint32_t>(x)), "r"(id)
+               : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// The units of this thread block, segment by segment: every role walks them on its own.
+struct Segment {
+  Group grp;
+  int g, rb, rows, bfirst;
+  u32 us, c, ce;      // first unit of the segment, this block's range of it
+  u32 slot;           // partial index
+};
+template <int G>
+struct Walk {
+  u32 c, c1, unit0, seg0;
+  int gr;
+  __device__ explicit Walk(const Plan& p) : c(blockIdx.x * p.Q), c1(min(blockIdx.x * p.Q + p.Q, p.total)), unit0(p.unit0), seg0(p.seg0), gr(p.group) {}
+  __device__ bool next(const DecodeArgs& a, Segment& s) {
+    while (c < c1) {
+      bool bad;
+      s.grp = load_group<G>(a, gr, &bad);
+      const u32 nseg = static_cast<u32>(a.Hkv) * s.grp.nrb;
+      if (s.grp.tiles == 0 || c >= unit0 + nseg * s.grp.tiles) {
+        if (s.grp.tiles) {
+          unit0 += nseg * s.grp.tiles;
+          seg0 += nseg;
+        }
+        ++gr;
+        continue;
+      }
+      const u32 sg = (c - unit0) / s.grp.tiles;
+      s.us = unit0 + sg * s.grp.tiles;
+      s.g = static_cast<int>(sg / s.grp.nrb);
+      s.rb = static_cast<int>(sg % s.grp.nrb);
+      s.rows = min(kRB, s.grp.n * G - s.rb * kRB);
+      s.bfirst = s.grp.b0 + s.rb * (kRB / G);
+      s.c = c;
+      s.ce = c = min(c1, s.us + s.grp.tiles);
+      s.slot = blockIdx.x + seg0 + sg;
+      return true;
+    }
+    return false;
+  }
+};
+
+// Row of the A operand's k order that dimension d takes (the order in which unpack_keys meets it).
+template <int D>
+__device__ __forceinline__ int key_order(int d) {
+  constexpr int NU = D / 64;
+  const int group = d >> 3, u = group >> 1, j = 2 * (group & 1) + (d & 1), pair = (d >> 1) & 1, hi = (d >> 2) & 1;
+  const int i = 8 * (u % NU) + 2 * j + pair;
+  return 2 * (4 * i + u / NU) + hi;
+}
+
+// Key codes of two tiles (this warp's 32 TMEM lanes) to fp16 subnormals: thread t reads pair-row t / 4
+// (rows t / 4 in the low nibbles, t / 4 + 8 in the high ones, kept as 16 c), 16 NU bytes of it; the
+// 8 lanes of a shared-memory phase read 8 different 16-byte units.
+template <int D>
+__device__ __forceinline__ void unpack_keys(const uint8_t* raw, uint32_t tmem, int w, int lane) {
+  constexpr int NU = D / 64;
+  const int pr = lane >> 2, q = lane & 3;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const uint8_t* row = raw + (2 * w + t) * Geo<D>::T4B + pr * D;
+#pragma unroll
+    for (int ul = 0; ul < NU; ++ul) {
+      const uint4 v = *reinterpret_cast<const uint4*>(row + 16 * ((NU * q + ul) ^ (D >= 128 ? (pr & 1) : 0)));
+      const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+      uint32_t r[16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = wd[j], hi = wd[j] >> 8;
+        r[4 * j + 0] = lo & 0x000F000Fu;
+        r[4 * j + 1] = lo & 0x00F000F0u;
+        r[4 * j + 2] = hi & 0x000F000Fu;
+        r[4 * j + 3] = hi & 0x00F000F0u;
+      }
+      tc::st_16x128b_x8(tmem + (static_cast<uint32_t>(32 * w + 16 * t) << 16) + 32 * ul, r);
+    }
+  }
+}
+
+// A position whose largest value z + 15 s is beyond fp16 (z and s are fp16, so it is below 16 times its
+// range): the unit's values are then taken times 1/16 and its probabilities times 16.  The warps
+// that unpack and the ones that form P find it each from the same bytes.
+__device__ __forceinline__ bool value_large(uint32_t sz) { return fmaf(15.f, half_lo(sz), half_hi(sz)) > 65504.f; }
+
+// Values of the unit to fp16, transposed: thread t takes quad Q = 8 w + t / 4 (4 dims) and the row
+// pairs 4 i + t % 4 of the unit; dim 4 Q + k goes to TMEM lane 32 w + 8 k + t / 4, row pair p to
+// column p.  Rows outside [lo, hi) may hold anything: their scale and zero are taken as 0.  With
+// `large` the values are taken times 1/16 (see value_large).
+template <int D>
+__device__ __forceinline__ void unpack_values(const uint8_t* raw, uint32_t tmem, int w, int lane, uint32_t ok, int lo, int hi, bool large) {
   using Gm = Geo<D>;
+  const int a = lane >> 2, q = lane & 3, Q = 8 * w + a;
+  const uint8_t* vw = raw + 8 * D + ((Q / Gm::WPC) * 4 + q) * Gm::CH + 4 * (Q % Gm::WPC);
+  const uint8_t* pp = raw + 16 * D + 64 + 8 * q;
+  const bool whole = ok == 0xFFu && lo <= 0 && hi >= kTile;
+  const __half2 sixteenth = __float2half2_rn(0.0625f);
+#pragma unroll
+  for (int blk = 0; blk < 2; ++blk) {  // 32 columns: 4 tiles
+    uint32_t r[2][16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int T = 4 * blk + (i >> 1), half = i & 1;
+      const uint32_t x = *reinterpret_cast<const uint32_t*>(vw + T * Gm::T4B + half * 32 * Gm::CH);
+      uint2 sz = *reinterpret_cast<const uint2*>(pp + T * Gm::T4B + half * 32);
+      if (!whole) {
+        const int p0 = 16 * T + 8 * half + 2 * q;
+        if (!((ok >> T) & 1u) || p0 < lo || p0 >= hi) sz.x = 0u;
+        if (!((ok >> T) & 1u) || p0 + 1 < lo || p0 + 1 >= hi) sz.y = 0u;
+      }
+      const uint32_t s2 = prmt(sz.x, sz.y, 0x5410u), z2 = prmt(sz.x, sz.y, 0x7632u);
+      __half2 s = *reinterpret_cast<const __half2*>(&s2), z = *reinterpret_cast<const __half2*>(&z2);
+      if (large) {
+        s = __hmul2(s, sixteenth);
+        z = __hmul2(z, sixteenth);
+      }
+      const uint32_t x8 = x >> 8;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        // 1024 + c or 1024 + 16 c, the exact code c, then one rounding of z + s c
+        const uint32_t src = k < 2 ? x : x8;
+        uint32_t h;
+        if (k & 1) asm("lop3.b32 %0, %1, 0x00F000F0, 0x64006400, 0xea;" : "=r"(h) : "r"(src));
+        else asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xea;" : "=r"(h) : "r"(src));
+        const __half2 m = *reinterpret_cast<const __half2*>(&h);
+        const __half2 n = (k & 1) ? __hfma2(m, sixteenth, __float2half2_rn(-64.f)) : __hadd2(m, __float2half2_rn(-1024.f));
+        const __half2 v = __hfma2(n, s, z);
+        r[k >> 1][2 * i + (k & 1)] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    }
+    tc::st_16x128b_x8(tmem + (static_cast<uint32_t>(32 * w) << 16) + 32 * blk, r[0]);
+    tc::st_16x128b_x8(tmem + (static_cast<uint32_t>(32 * w + 16) << 16) + 32 * blk, r[1]);
+  }
+}
+
+template <int D, int G, int QT>
+__global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const DecodeArgs a) {
+  using Gm = Geo<D>;
+  using C = Cols<D>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   SmemPrefix<D>& sm = *reinterpret_cast<SmemPrefix<D>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cap = a.stride * a.P;
+  volatile int* abort = &sm.abort;
   pdl_wait();
   if (warp == 0) make_plan<G>(a, lane, sm.plan);
-  __syncthreads();
-  write_rows<G>(a, sm.plan);
-  const u32 Q = sm.plan.Q;
-  u32 c = blockIdx.x * Q;
-  const u32 c1 = min(c + Q, sm.plan.total);
-  int gr = sm.plan.group;
-  u32 unit0 = sm.plan.unit0, seg0 = sm.plan.seg0;
-  while (c < c1) {
-    bool bad;
-    const Group grp = load_group<G>(a, gr, &bad);
-    const u32 nseg = static_cast<u32>(a.Hkv) * grp.nrb;
-    if (grp.tiles == 0 || c >= unit0 + nseg * grp.tiles) {
-      if (grp.tiles) {
-        unit0 += nseg * grp.tiles;
-        seg0 += nseg;
-      }
-      ++gr;
-      continue;
+  if (tid == 32) {
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(&sm.raw_full[i], 1);
+      mbar_init(&sm.raw_empty[i], 16);
     }
-    const u32 sg = (c - unit0) / grp.tiles;
-    const u32 us = unit0 + sg * grp.tiles;  // first unit of the segment
-    const int g = static_cast<int>(sg / grp.nrb), rb = static_cast<int>(sg % grp.nrb);
-    const int rows = min(kRB, grp.n * G - rb * kRB);
-    const int bfirst = grp.b0 + rb * (kRB / G);
-    const u32 ce = min(c1, us + grp.tiles);
-    // queries
-    for (int r = warp; r < kRB; r += kPrefixThreads / 32) {
-      const int b = bfirst + r / G;
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
-      const bool act = lane < D / 4;
-      if (r < rows && act) {
-        const size_t q0 = (static_cast<size_t>(b) * a.Hq + static_cast<size_t>(g) * G + r % G) * D + 4 * lane;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = load_q<QT>(a.q, q0 + e);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.k_ready[i], 4);
+      mbar_init(&sm.v_ready[i], 4);
+      mbar_init(&sm.qk_done[i], 1);
+      mbar_init(&sm.s_free[i], kSoftWarps);
+      mbar_init(&sm.p_ready[i], kSoftWarps);
+      mbar_init(&sm.pv_done[i], 1);
+    }
+    mbar_init(&sm.q_ready, kSoftWarps);
+    mbar_init(&sm.stall, 1);
+    fence_mbar_init();
+    sm.abort = 0;
+  }
+  if (warp == kMmaWarp) tc::alloc(&sm.tmem, C::All);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tm = sm.tmem;
+  auto wait = [&](uint64_t* bar, u32 n) { wait_bar(bar, n & 1u, abort, a.err, a.wait_ns); };  // the n-th completion (0-based)
+
+  Walk<G> walk(sm.plan);
+  Segment s;
+  u32 i = 0;  // units so far
+  const int s16 = a.s >> 4;
+
+  if (warp < kSoftWarps) {
+    // ------------------------------------------------------------------ softmax
+    const int wg = warp >> 2, w4 = warp & 3, pos = 32 * w4 + lane, id = 1 + wg;
+    const uint32_t quad = static_cast<uint32_t>(32 * w4) << 16;
+    if (a.stall_test) wait(&sm.stall, 0);
+    while (walk.next(a, s)) {
+      // the segment's queries, rotated, in log2 units: 8 rows a warp
+      if (tid == 0) {
+        sm.edge[0] = 0x7fffffff;
+        sm.edge[1] = 0;
+        sm.scaled = 0;
       }
-      flip_signs4(x, lane, a.signs);
-      hadamard4(x, lane, a.h);
-      if (act) {
+      asm volatile("barrier.cta.sync 3, 256;" ::: "memory");
+      for (int r = warp; r < kRB; r += kSoftWarps) {
+        const int b = s.bfirst + r / G;
+        const bool act = lane < D / 4;
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        if (r < s.rows && act) {
+          const size_t q0 = (static_cast<size_t>(b) * a.Hq + static_cast<size_t>(s.g) * G + r % G) * D + 4 * lane;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = load_q<QT>(a.q, q0 + e);
+        }
+        flip_signs4(x, lane, a.signs);
+        hadamard4(x, lane, a.h);
+        float big = 0.f, sum = 0.f, f = 1.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          sm.q[r][4 * lane + e] = x[e] * (a.qscale / a.h);
-          sm.o[r][4 * lane + e] = 0.f;
+          x[e] *= a.qscale * kQShift / a.h;
+          big = fmaxf(big, fabsf(x[e]));
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(FULL, big, o));
+        if (big > 32768.f) {  // beyond fp16: down by a power of two (2^100 at most), undone on the logits
+          const int ex = min(((__float_as_int(big) >> 23) & 0xff) - 127 - 14, 100);
+          f = __int_as_float((127 + ex) << 23);
+          const float down = __int_as_float((127 - ex) << 23);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] *= down;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half hx = __float2half_rn(x[e]);
+          sum += __half2float(hx);
+          const int k = key_order<D>(4 * lane + e);
+          if (act) sm.Q[(k >> 3) * (kRB * 8) + r * 8 + (k & 7)] = hx;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+        if (lane == 0) {
+          float* c = reinterpret_cast<float*>(&sm.cst[r >> 1]);
+          c[r & 1] = sum * (1.f / kQShift);
+          c[2 + (r & 1)] = r < s.rows ? -kUnset : 0.f;
+          reinterpret_cast<float*>(sm.mul)[r] = f;
+          const int lim = r < s.rows ? min(16 * s.grp.te, max(a.s, clamp_len(a.lens[b], cap) - a.w)) : 0;
+          sm.lim[r] = lim;
+          if (r < s.rows) {
+            atomicMin(&sm.edge[0], lim);
+            atomicMax(&sm.edge[1], lim);
+          }
+          if (f != 1.f) sm.scaled = 1;
         }
       }
-      if (lane == 0) {
-        sm.m[r] = kNegInf;
-        sm.l[r] = 0.f;
-        sm.lim[r] = r < rows ? min(16 * grp.te, max(a.s, clamp_len(a.lens[b], cap) - a.w)) : 0;
+      if (s.c == s.us) {
+        const u32 last = (s.us + s.grp.tiles - 1) / sm.plan.Q;
+        for (int k = tid; k * G < s.rows; k += 256)
+          a.pmeta[(s.bfirst + k) * a.Hkv + s.g] = make_uint4(s.slot, last - blockIdx.x + 1, k * G, 0u);
       }
-    }
-    if (c == us) {
-      const u32 last = (us + grp.tiles - 1) / Q;
-      for (int i = tid; i * G < rows; i += kPrefixThreads)
-        a.pmeta[(bfirst + i) * a.Hkv + g] = make_uint4(blockIdx.x + seg0 + sg, last - blockIdx.x + 1, i * G, 0u);
-    }
-    __syncthreads();
-    for (; c < ce; ++c) {
-      const int t0 = (a.s >> 4) + static_cast<int>(c - us) * (kTile / 16);  // first 16-position tile
-      for (int i = tid; i < kTile * D; i += kPrefixThreads) {
-        const int pos = i / D, d = i % D, ti = t0 + (pos >> 4), r = pos & 15;
-        float k = 0.f, v = 0.f;
-        if (ti < grp.te) {
-          int lp, tin;
-          tile_page(a, ti, &lp, &tin);
-          const int page = a.page_table[static_cast<size_t>(grp.b0) * a.stride + lp];
-          if (page >= 0 && page < a.max_pages) {
-            uint8_t* tile = const_cast<uint8_t*>(a.pool) + static_cast<size_t>(page) * a.page_bytes +
-                            (static_cast<size_t>(g) * (a.P / 16) + tin) * Gm::T4B;
-            const uint32_t kp = *reinterpret_cast<const uint32_t*>(tile + 16 * D + 4 * r);
-            const uint32_t vp = *reinterpret_cast<const uint32_t*>(tile + 16 * D + 64 + 4 * r);
-            const uint32_t kw = k4_words<D>(tile, r & 7, d >> 2)[d & 1] >> (16 * ((d >> 2) & 1) + 4 * (r >> 3) + 8 * ((d >> 1) & 1));
-            k = fmaf(half_lo(kp), static_cast<float>(kw & 15u), half_hi(kp));
-            v = fmaf(half_lo(vp), static_cast<float>((*v4_chunk<D>(tile, r, d >> 2) >> (4 * (d & 3))) & 15), half_hi(vp));
-          } else if (d == 0 && r == 0) {
-            atomicOr(a.err, KV4_DEVERR_PAGE_RANGE);
+      fence_proxy_async_smem();
+      asm volatile("barrier.cta.sync 3, 256;" ::: "memory");
+      warp_arrive(&sm.q_ready, lane);
+      const int lim_min = sm.edge[0], lim_max = sm.edge[1];
+      const bool scaled = sm.scaled != 0;
+      const int ncol = min(32, max(0, ((s.rows + 15) & ~15) - 32 * wg));  // 0, 16 or 32
+      float l[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) l[j] = 0.f;
+
+      const u32 i0 = i;
+      for (u32 c = s.c; c < s.ce; ++c, ++i) {
+        const int t0 = s16 + static_cast<int>(c - s.us) * (kTile / 16);
+        const int st = static_cast<int>(i % kRaw), bf = static_cast<int>(i & 1);
+        wait(&sm.raw_full[st], i / kRaw);
+        const uint32_t kp = *reinterpret_cast<const uint32_t*>(sm.raw[st] + (pos >> 4) * Gm::T4B + 16 * D + 4 * (pos & 15));
+        const uint32_t vp = *reinterpret_cast<const uint32_t*>(sm.raw[st] + (pos >> 4) * Gm::T4B + 16 * D + 64 + 4 * (pos & 15));
+        const bool here = (sm.ok[st] >> (pos >> 4)) & 1u;
+        warp_arrive(&sm.raw_empty[st], lane);
+        // codes are c 2^-24 (rows 8-15 of a tile: 16 c 2^-24), queries times kQShift
+        const float ks = half_lo(kp) * ((pos & 8) ? 1048576.f / kQShift : 16777216.f / kQShift), kz = half_hi(kp);
+        const int at = 16 * t0 + pos;
+        const bool dead = !here || at < a.s;
+        const bool large = !dead && at < lim_max && value_large(vp);
+        const bool edge = 16 * t0 < a.s || 16 * t0 + kTile > lim_min || sm.ok[st] != 0xFFu;
+        wait(&sm.qk_done[bf], i >> 1);
+        tc::fence_after();
+
+        float e[32];
+        const uint64_t ks2 = tc::pack2(ks, ks), kz2 = tc::pack2(kz, kz);
+        // logits minus the running maximum (whole: the logits themselves)
+        auto logits = [&](bool minus) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (16 * h >= ncol) break;
+            uint32_t sreg[16];
+            tc::ld16(tm + quad + C::S + kRB * bf + 32 * wg + 16 * h, sreg);
+            tc::wait_ld();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int n2 = 16 * wg + 8 * h + j;
+              const float4 cc = sm.cst[n2];
+              const uint64_t sv = tc::pack2(__uint_as_float(sreg[2 * j]), __uint_as_float(sreg[2 * j + 1]));
+              const uint64_t off = minus ? tc::pack2(cc.z, cc.w) : 0ull;
+              uint64_t x;
+              if (!scaled) {
+                x = tc::fma2(ks2, sv, tc::fma2(kz2, tc::pack2(cc.x, cc.y), off));
+              } else {
+                const float2 f = sm.mul[n2];
+                x = tc::fma2(tc::pack2(f.x, f.y), tc::fma2(ks2, sv, tc::mul2(kz2, tc::pack2(cc.x, cc.y))), off);
+              }
+              tc::unpack2(x, e[16 * h + 2 * j], e[16 * h + 2 * j + 1]);
+              if (edge) {
+                if (dead || at >= sm.lim[2 * n2]) e[16 * h + 2 * j] = kNegInf;
+                if (dead || at >= sm.lim[2 * n2 + 1]) e[16 * h + 2 * j + 1] = kNegInf;
+              }
+            }
+          }
+        };
+        logits(true);
+        float top = kNegInf;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if ((j & ~15) < ncol) top = fmaxf(top, e[j]);
+        float lmul = 1.f;
+        if (ncol && group_or(id, top > kGrow || large)) {
+          const bool times16 = group_or(id, large);
+          // raise the running maxima to this unit's: column maxima over the 128 positions
+          logits(false);
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = (j & ~15) < ncol ? e[j] : kNegInf;
+#pragma unroll
+          for (int o = 16; o; o >>= 1)
+#pragma unroll
+            for (int j = 0; j < o; ++j) {
+              const bool up = (lane & o) != 0;
+              const float got = __shfl_xor_sync(FULL, up ? v[j] : v[j + o], o);
+              v[j] = fmaxf(up ? v[j + o] : v[j], got);
+            }
+          sm.red[wg][w4][lane] = v[0];
+          group_sync(id);
+          if (w4 == 0) {
+            const int n = 32 * wg + lane;
+            float* neg = reinterpret_cast<float*>(&sm.cst[n >> 1]) + 2 + (n & 1);
+            const float m0 = -*neg;
+            const float m1 = fmaxf(fmaxf(sm.red[wg][0][lane], sm.red[wg][1][lane]), fmaxf(sm.red[wg][2][lane], sm.red[wg][3][lane]));
+            const bool raise = lane < ncol && m1 > m0;
+            sm.alpha[n] = !raise ? 1.f : m0 == kUnset ? 0.f : exp2_fast(m0 - m1);
+            if (raise) *neg = -m1;
+          }
+          group_sync(id);
+          if (i > i0) {  // outputs so far: after the MMAs that are adding to them
+            wait(&sm.pv_done[(i - 1) & 1], (i - 1) >> 1);
+            tc::fence_after();
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (16 * h >= ncol) break;
+            uint32_t o[16];
+            const uint32_t addr = tm + quad + C::O + 32 * wg + 16 * h;
+            if (i > i0) {
+              tc::ld16(addr, o);
+              tc::wait_ld();
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float al = sm.alpha[32 * wg + 16 * h + j];
+              l[16 * h + j] *= al;
+              o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
+            }
+            if (i > i0) tc::st16(addr, o);
+          }
+          tc::wait_st();
+          logits(true);
+          if (times16) {
+            lmul = 0.0625f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if ((j & ~15) < ncol) e[j] += 4.f;
           }
         }
-        sm.K[pos][d] = k;
-        sm.V[pos][d] = v;
+        tc::fence_before();
+        warp_arrive(&sm.s_free[bf], lane);
+        if (i >= 2) wait(&sm.pv_done[bf], (i >> 1) - 1);  // the buffer's last product
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          if (8 * h >= ncol) break;
+          uint32_t pk[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float p0 = exp2_fast(e[8 * h + 2 * j]), p1 = exp2_fast(e[8 * h + 2 * j + 1]);
+            l[8 * h + 2 * j] = fmaf(p0, lmul, l[8 * h + 2 * j]);
+            l[8 * h + 2 * j + 1] = fmaf(p1, lmul, l[8 * h + 2 * j + 1]);
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[j]) : "f"(p1), "f"(p0));
+          }
+          *reinterpret_cast<uint4*>(&sm.P[bf][(4 * wg + h) * (kTile * 8) + pos * 8]) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
+        fence_proxy_async_smem();
+        tc::fence_before();
+        warp_arrive(&sm.p_ready[bf], lane);
       }
-      __syncthreads();
-      for (int r = warp; r < rows; r += kPrefixThreads / 32) {
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int d = 0; d < D; ++d) {
-          const float qv = sm.q[r][d];
+
+      // the segment's partial: O^T lane 8 k + a of this warp is dim 32 w4 + 4 a + k
+      wait(&sm.pv_done[(i - 1) & 1], (i - 1) >> 1);
+      tc::fence_after();
+      float* part = a.ppart + static_cast<size_t>(s.slot) * kRB * kPartRow<D>;
+      const int dim = 32 * w4 + 4 * (lane & 7) + (lane >> 3);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = fmaf(qv, sm.K[lane + 32 * i][d], x[i]);
+      for (int h = 0; h < 2; ++h) {
+        if (16 * h >= ncol) break;
+        uint32_t o[16];
+        tc::ld16(tm + quad + C::O + 32 * wg + 16 * h, o);
+        tc::wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int n = 32 * wg + 16 * h + j;
+          if (n < s.rows && dim < D) part[n * kPartRow<D> + dim] = __uint_as_float(o[j]);
         }
-        float mx = kNegInf;
+      }
+      if (ncol) {
+        // sums over the 128 positions
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int pos = 16 * t0 + lane + 32 * i;
-          if (pos < a.s || pos >= sm.lim[r]) x[i] = kNegInf;
-          mx = fmaxf(mx, x[i]);
+        for (int o = 16; o; o >>= 1)
+#pragma unroll
+          for (int j = 0; j < o; ++j) {
+            const bool up = (lane & o) != 0;
+            const float got = __shfl_xor_sync(FULL, up ? l[j] : l[j + o], o);
+            l[j] = (up ? l[j + o] : l[j]) + got;
+          }
+        sm.red[wg][w4][lane] = l[0];
+        group_sync(id);
+        const int n = 32 * wg + lane;
+        if (w4 == 0 && n < s.rows) {
+          const float m = -(reinterpret_cast<const float*>(&sm.cst[n >> 1])[2 + (n & 1)]);
+          *reinterpret_cast<float2*>(part + n * kPartRow<D> + D) =
+              make_float2(m, (sm.red[wg][0][lane] + sm.red[wg][1][lane]) + (sm.red[wg][2][lane] + sm.red[wg][3][lane]));
         }
+      }
+      tc::fence_before();
+      asm volatile("barrier.cta.sync 3, 256;" ::: "memory");
+    }
+  } else if (warp < kValWarp0) {
+    // ------------------------------------------------------------------ keys
+    const int w = warp - kKeyWarp0;
+    while (walk.next(a, s))
+      for (u32 c = s.c; c < s.ce; ++c, ++i) {
+        const int st = static_cast<int>(i % kRaw), bf = static_cast<int>(i & 1);
+        wait(&sm.raw_full[st], i / kRaw);
+        if (i >= 2) wait(&sm.qk_done[bf], (i >> 1) - 1);
+        tc::fence_after();
+        unpack_keys<D>(sm.raw[st], tm + C::K + (D / 2) * bf, w, lane);
+        warp_arrive(&sm.raw_empty[st], lane);
+        tc::wait_st();
+        tc::fence_before();
+        warp_arrive(&sm.k_ready[bf], lane);
+      }
+  } else if (warp < kCopyWarp) {
+    // ------------------------------------------------------------------ values
+    const int w = warp - kValWarp0;
+    while (walk.next(a, s)) {
+      // positions that some row attends (others may be unwritten)
+      int hi = 0;
+      for (int r = lane; r * G < s.rows; r += 32) hi = max(hi, clamp_len(a.lens[s.bfirst + r], cap) - a.w);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
-        const float mo = sm.m[r], mn = fmaxf(mo, mx);
-        if (mn == kNegInf) continue;
-        const float alpha = mo == kNegInf ? 0.f : exp2f(mo - mn);
-        float ls = 0.f;
+      for (int o = 16; o; o >>= 1) hi = max(hi, __shfl_xor_sync(FULL, hi, o));
+      hi = min(hi, 16 * s.grp.te);
+      for (u32 c = s.c; c < s.ce; ++c, ++i) {
+        const int st = static_cast<int>(i % kRaw), bf = static_cast<int>(i & 1);
+        const int p0 = 16 * (s16 + static_cast<int>(c - s.us) * (kTile / 16));
+        wait(&sm.raw_full[st], i / kRaw);
+        if (i >= 2) wait(&sm.pv_done[bf], (i >> 1) - 1);
+        tc::fence_after();
+        const uint32_t ok = sm.ok[st];
+        if (32 * w < D) {
+          const uint4 vp = *reinterpret_cast<const uint4*>(sm.raw[st] + (lane >> 2) * Gm::T4B + 16 * D + 64 + 16 * (lane & 3));
+          const uint32_t v4[4] = {vp.x, vp.y, vp.z, vp.w};
+          bool large = false;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float pv = exp2f(x[i] - mn);
-          sm.p[warp][lane + 32 * i] = pv;
-          ls += pv;
+          for (int e = 0; e < 4; ++e) {
+            const int at = p0 + 4 * lane + e;
+            large |= ((ok >> (lane >> 2)) & 1u) && at >= a.s && at < hi && value_large(v4[e]);
+          }
+          unpack_values<D>(sm.raw[st], tm + C::V + (kTile / 2) * bf, w, lane, ok, a.s - p0, hi - p0, __any_sync(FULL, large));
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(FULL, ls, o);
-        __syncwarp();
-        for (int d = lane; d < D; d += 32) {
-          float acc = sm.o[r][d] * alpha;
-          for (int t = 0; t < kTile; ++t)
-            if (sm.p[warp][t] != 0.f) acc = fmaf(sm.p[warp][t], sm.V[t][d], acc);
-          sm.o[r][d] = acc;
-        }
+        warp_arrive(&sm.raw_empty[st], lane);
+        tc::wait_st();
+        tc::fence_before();
+        warp_arrive(&sm.v_ready[bf], lane);
+      }
+    }
+  } else if (warp == kCopyWarp) {
+    // ------------------------------------------------------------------ copies
+    auto page_of = [&](int ti) {  // page of a 16-position tile; the next unit's is read one unit ahead
+      int lp, tin;
+      tile_page(a, ti, &lp, &tin);
+      return ti < s.grp.te ? a.page_table[static_cast<size_t>(s.grp.b0) * a.stride + lp] : 0;
+    };
+    while (walk.next(a, s)) {
+      int page = lane < 8 ? page_of(s16 + static_cast<int>(s.c - s.us) * 8 + lane) : 0;
+      for (u32 c = s.c; c < s.ce; ++c, ++i) {
+        const int st = static_cast<int>(i % kRaw);
+        const int ti = s16 + static_cast<int>(c - s.us) * 8 + lane;
+        const int next = (lane < 8 && c + 1 < s.ce) ? page_of(ti + 8) : 0;
+        if (i >= kRaw) wait(&sm.raw_empty[st], i / kRaw - 1);
+        const bool in = lane < 8 && ti < s.grp.te, good = in && page >= 0 && page < a.max_pages && !*abort;
+        if (in && !good && !*abort) atomicOr(a.err, KV4_DEVERR_PAGE_RANGE);
+        const uint32_t ok = __ballot_sync(FULL, good);
         if (lane == 0) {
-          sm.m[r] = mn;
-          sm.l[r] = sm.l[r] * alpha + ls;
+          sm.ok[st] = ok;
+          mbar_arrive_expect_tx(&sm.raw_full[st], __popc(ok) * Gm::T4B);
         }
         __syncwarp();
+        if (good) {
+          int lp, tin;
+          tile_page(a, ti, &lp, &tin);
+          bulk_g2s(sm.raw[st] + lane * Gm::T4B,
+                   a.pool + static_cast<size_t>(page) * a.page_bytes + (static_cast<size_t>(s.g) * (a.P / 16) + tin) * Gm::T4B, Gm::T4B,
+                   &sm.raw_full[st]);
+        }
+        page = next;
       }
-      __syncthreads();
     }
-    float* part = a.ppart + static_cast<size_t>(blockIdx.x + seg0 + sg) * kRB * kPartRow<D>;
-    for (int i = tid; i < rows * D; i += kPrefixThreads) part[(i / D) * kPartRow<D> + i % D] = sm.o[i / D][i % D];
-    for (int r = tid; r < rows; r += kPrefixThreads) {
-      part[r * kPartRow<D> + D] = sm.m[r];
-      part[r * kPartRow<D> + D + 1] = sm.l[r];
+    // no copy outlives the block
+    for (u32 k = i > kRaw ? i - kRaw : 0; k < i; ++k) mbar_wait_bounded(&sm.raw_full[k % kRaw], (k / kRaw) & 1u, a.err, kWaitLimitNs);
+    write_rows<G>(a, sm.plan, lane);
+  } else {
+    // ------------------------------------------------------------------ matrix products
+    if (lane == 0) {
+      const uint32_t q0 = smem_u32(sm.Q), p0 = smem_u32(sm.P);
+      u32 seg = 0, first = 0;
+      uint32_t nmma = 0;
+      auto pv = [&](u32 k, bool acc) {  // products of unit k
+        const int bf = static_cast<int>(k & 1);
+        wait(&sm.p_ready[bf], k >> 1);
+        wait(&sm.v_ready[bf], k >> 1);
+        tc::fence_after();
+        if (!*abort) {
+          const uint32_t id = tc::idesc_f16(kTile, nmma, true);
+#pragma unroll
+          for (int x = 0; x < kTile / 16; ++x)
+            tc::mma_ts(tm + C::O, tm + C::V + (kTile / 2) * bf + 8 * x, tc::smem_desc(p0 + bf * (kRB * kTile * 2) + x * 256, 128, kTile * 16), id,
+                       acc || x > 0);
+        }
+        tc::commit(&sm.pv_done[bf]);
+      };
+      while (walk.next(a, s)) {
+        first = i;
+        wait(&sm.q_ready, seg++);
+        nmma = static_cast<uint32_t>((s.rows + 15) & ~15);
+        const uint32_t id = tc::idesc_f16(kTile, nmma, false);
+        for (u32 c = s.c; c < s.ce; ++c, ++i) {
+          const int bf = static_cast<int>(i & 1);
+          wait(&sm.k_ready[bf], i >> 1);
+          if (i >= 2) wait(&sm.s_free[bf], (i >> 1) - 1);
+          tc::fence_after();
+          if (!*abort) {
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x)
+              tc::mma_ts(tm + C::S + kRB * bf, tm + C::K + (D / 2) * bf + 8 * x, tc::smem_desc(q0 + x * (2 * kRB * 16), kRB * 16, 128), id, x > 0);
+          }
+          tc::commit(&sm.qk_done[bf]);
+          if (i > first) pv(i - 1, i - 1 > first);
+        }
+        pv(i - 1, i - 1 > first);
+      }
+      // the last products are done before TMEM is freed, however the loop ended
+      for (u32 k = i > 2 ? i - 2 : 0; k < i; ++k) {
+        mbar_wait_bounded(&sm.qk_done[k & 1], (k >> 1) & 1u, a.err, kWaitLimitNs);
+        mbar_wait_bounded(&sm.pv_done[k & 1], (k >> 1) & 1u, a.err, kWaitLimitNs);
+      }
     }
-    __syncthreads();
+    __syncwarp();
   }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == kMmaWarp) tc::dealloc(tm, C::All);
 }
 
 // ------------------------------------------------------------------ merge of prefix and own partials

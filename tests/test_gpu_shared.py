@@ -327,3 +327,25 @@ def test_workspace_too_small(kv4):
     with pytest.raises(kv4.KV4Error) as e:
         r.cache.decode_shared(0, r.q, r.pt, r.lens, r.start_d, r.prefix_d, workspace=torch.empty(n - 16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == kv4.KV4_ERR_WORKSPACE
+
+
+@gpu
+def test_values_beyond_fp16(kv4):
+    """A value vector whose INT4 scale reaches values past the fp16 range, among ordinary ones."""
+    r = build(CASES[0], kv4)
+    L, hot = 240, 133
+    wl = r.wl
+    b = np.zeros(2, np.int32)
+    p = np.array([hot, 70], np.int32)
+    K, V = wl.kv_inputs(0, b, p)
+    V[0] = np.linspace(-60000.0, 500000.0, V[0].size).reshape(V[0].shape)
+    V[1] = np.linspace(3e-4, 5e-4, V[1].size).reshape(V[1].shape)
+    K[0] = -20 * wl.kv_inputs(0, b[:1], p[:1])[0][0]
+    keep = r.side.copy()
+    O.append(r.cfg, r.pool, r.side, K, V, b, p, wl.lens, wl.page_table)
+    assert np.array_equal(keep, r.side)
+    r.cache.layer_views(0)[0].copy_(torch.from_numpy(r.pool))
+    want = reference(r)
+    out = r.cache.decode_shared(0, r.q, r.pt, r.lens, r.start_d, r.prefix_d, out=torch.empty(r.q.shape, device="cuda"))
+    assert np.isfinite(want[0]).all() and want[2].max() < 1e5
+    check(r, out, None, want)
