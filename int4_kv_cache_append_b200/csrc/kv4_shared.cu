@@ -12,7 +12,7 @@
 // Keeping A in TMEM leaves shared memory to the packed tiles, Q and P; with the positions as the
 // MMA's rows its cost follows the number of query rows, and s_t and z_t are one thread's constants.
 //
-// A thread block is 18 warps: two softmax warpgroups (32 of the 64 columns each, a thread per
+// A thread block is 26 warps: four softmax warpgroups (16 of the 64 columns each, a thread per
 // position), a warpgroup unpacking keys, one unpacking values, a warp of bulk copies and a warp
 // that issues the MMAs; K, V, S and P have two buffers, the packed tiles four.  The running maximum
 // of a row is raised only when a logit exceeds it by more than 8 (P then stays below 2^8, far inside
@@ -147,8 +147,10 @@ __device__ void write_rows(const DecodeArgs& a, const Plan& p, int lane) {
 
 // ------------------------------------------------------------------ prefix attention
 
-constexpr int kSoftWarps = 8, kKeyWarp0 = 8, kValWarp0 = 12, kCopyWarp = 16, kMmaWarp = 17;
-constexpr int kPrefixThreads = 18 * 32;
+constexpr int kSoftGroups = 4;   // softmax warpgroups: group g takes the 8-column chunks g and g + 4
+constexpr int kSoftWarps = 4 * kSoftGroups, kKeyWarp0 = kSoftWarps, kValWarp0 = kKeyWarp0 + 4, kCopyWarp = kValWarp0 + 4,
+              kMmaWarp = kCopyWarp + 1, kSoftThreads = 32 * kSoftWarps;
+constexpr int kPrefixThreads = 32 * (kMmaWarp + 1);
 constexpr float kUnset = -1e30f;   // running maximum of a row that has seen no position
 constexpr float kGrow = 8.f;       // a logit this far above the running maximum raises it
 constexpr float kQShift = 64.f;    // queries enter fp16 times this: typical ones are then near one
@@ -159,11 +161,13 @@ struct SmemPrefix {
   __half P[2][kRB * kTile];   // [row / 8][position][row % 8]: MN-major core matrices
   __half Q[kRB * D];          // [k / 8][row][k % 8]: K-major core matrices
   float4 cst[kRB / 2];        // rows 2j, 2j + 1: sum(q), sum(q), -m, -m
-  float2 mul[kRB / 2];        // rows whose query had to be scaled down to fit fp16: the factor back
-  float alpha[kRB];
-  float red[2][4][32];
+  alignas(8) float mul[kRB];             // rows whose query had to be scaled down to fit fp16: the factor back
+  alignas(16) float alpha[kRB];
+  float red[kSoftGroups][4][16];
+  float2 ksz[kRaw][kTile];    // key scale (times the codes' and queries' powers of two) and zero
+  alignas(16) uint32_t large[kRaw][4];    // the unit has values beyond fp16 (one word per warp that looked)
   int lim[kRB];               // end of the row's INT4 positions in the prefix
-  int edge[2];                // smallest and largest lim of the rows
+  int edge;                   // smallest lim of the rows
   int scaled;                 // some row has mul != 1
   uint32_t ok[kRaw];          // tiles of the buffer that were copied
   uint64_t raw_full[kRaw], raw_empty[kRaw];
@@ -183,18 +187,21 @@ struct Cols {
 };
 
 // A bounded wait that gives up when any warp of the block has: every role then runs its loop to the
-// end without waiting, so that all of them reach the end of the kernel.
+// end without waiting, so that all of them reach the end of the kernel.  Short, because every role
+// has copies of it and they all run from one instruction cache; the clock is read every 64 polls.
 __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err, uint64_t limit_ns) {
-  if (mbar_try_wait(bar, parity)) return;
-  if (*abort) return;
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t it = 1; it < kWaitLimitPolls; ++it) {
-    if (mbar_try_wait(bar, parity)) return;
-    if ((it & 15u) == 0u && (*abort || global_timer_ns() - t0 > limit_ns)) break;
-  }
-  if (!*abort) {
-    *abort = 1;
-    atomicOr(err, KV4_DEVERR_WAIT_LIMIT);
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+    if (it & 63u) continue;
+    const uint64_t t = global_timer_ns();
+    if (t0 == 0) t0 = t;
+    if (*abort) return;
+    if (t - t0 > limit_ns || it >= kWaitLimitPolls) {
+      *abort = 1;
+      atomicOr(err, KV4_DEVERR_WAIT_LIMIT);
+      return;
+    }
   }
 }
 
@@ -206,7 +213,7 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   if (lane == 0) arrive(bar);
 }
 
-// One of the two softmax warpgroups in step, with the OR of a predicate.
+// One of the softmax warpgroups in step, with the OR of a predicate.
 __device__ __forceinline__ bool group_or(int id, bool x) {
   uint32_t r;
   asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 q, %1, 0;\n barrier.cta.red.or.pred p, %2, 128, q;\n selp.b32 %0, 1, 0, p;\n}\n"
@@ -215,6 +222,7 @@ __device__ __forceinline__ bool group_or(int id, bool x) {
                : "memory");
   return r != 0;
 }
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 5, %0;" ::"n"(kSoftThreads) : "memory"); }
 __device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
 
 // The units of this thread block, segment by segment: every role walks them on its own.
@@ -257,6 +265,16 @@ struct Walk {
   }
 };
 
+// End of the positions that some row of the segment attends; those past it may be unwritten.
+template <int G>
+__device__ __forceinline__ int attended_end(const DecodeArgs& a, const Segment& s, int cap, int lane) {
+  int hi = 0;
+  for (int r = lane; r * G < s.rows; r += 32) hi = max(hi, clamp_len(a.lens[s.bfirst + r], cap) - a.w);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) hi = max(hi, __shfl_xor_sync(FULL, hi, o));
+  return min(hi, 16 * s.grp.te);
+}
+
 // Row of the A operand's k order that dimension d takes (the order in which unpack_keys meets it).
 template <int D>
 __device__ __forceinline__ int key_order(int d) {
@@ -273,7 +291,7 @@ template <int D>
 __device__ __forceinline__ void unpack_keys(const uint8_t* raw, uint32_t tmem, int w, int lane) {
   constexpr int NU = D / 64;
   const int pr = lane >> 2, q = lane & 3;
-#pragma unroll
+#pragma unroll 1
   for (int t = 0; t < 2; ++t) {
     const uint8_t* row = raw + (2 * w + t) * Geo<D>::T4B + pr * D;
 #pragma unroll
@@ -311,7 +329,8 @@ __device__ __forceinline__ void unpack_values(const uint8_t* raw, uint32_t tmem,
   const uint8_t* pp = raw + 16 * D + 64 + 8 * q;
   const bool whole = ok == 0xFFu && lo <= 0 && hi >= kTile;
   const __half2 sixteenth = __float2half2_rn(0.0625f);
-#pragma unroll
+  // the unit's instructions are few: the warps of all roles run from one instruction cache
+#pragma unroll 1
   for (int blk = 0; blk < 2; ++blk) {  // 32 columns: 4 tiles
     uint32_t r[2][16];
 #pragma unroll
@@ -320,9 +339,9 @@ __device__ __forceinline__ void unpack_values(const uint8_t* raw, uint32_t tmem,
       const uint32_t x = *reinterpret_cast<const uint32_t*>(vw + T * Gm::T4B + half * 32 * Gm::CH);
       uint2 sz = *reinterpret_cast<const uint2*>(pp + T * Gm::T4B + half * 32);
       if (!whole) {
-        const int p0 = 16 * T + 8 * half + 2 * q;
-        if (!((ok >> T) & 1u) || p0 < lo || p0 >= hi) sz.x = 0u;
-        if (!((ok >> T) & 1u) || p0 + 1 < lo || p0 + 1 >= hi) sz.y = 0u;
+        const int p0 = 16 * T + 8 * half + 2 * q, h = ((ok >> T) & 1u) ? hi : 0;
+        if (p0 < lo || p0 >= h) sz.x = 0u;
+        if (p0 + 1 < lo || p0 + 1 >= h) sz.y = 0u;
       }
       const uint32_t s2 = prmt(sz.x, sz.y, 0x5410u), z2 = prmt(sz.x, sz.y, 0x7632u);
       __half2 s = *reinterpret_cast<const __half2*>(&s2), z = *reinterpret_cast<const __half2*>(&z2);
@@ -349,6 +368,56 @@ __device__ __forceinline__ void unpack_values(const uint8_t* raw, uint32_t tmem,
   }
 }
 
+// Raise the running maxima of softmax group wg's columns (nch chunks of 8) to this unit's: column
+// maxima over the 128 positions of its threads, factors for what was summed so far to sm.alpha
+// (outputs in TMEM are rescaled here, after the MMAs that are adding to them).  Seldom taken, kept
+// out of the loop.  s_addr, o_addr: scores and outputs of this warp's TMEM lanes.
+template <int D>
+__device__ __noinline__ void raise_maxima(SmemPrefix<D>& sm, int wg, int w4, int lane, uint32_t s_addr, uint32_t o_addr, int nch, float ks,
+                                          float kz, int at, bool dead, bool first) {
+  const int id = 1 + wg;
+#pragma unroll 1
+  for (int k = 0; k < nch; ++k) {
+    const int c0 = 8 * (wg + kSoftGroups * k);
+    uint32_t r[8];
+    tc::ld8(s_addr + c0, r);
+    tc::wait_ld(r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int n = c0 + j;
+      float x = fmaf(ks, __uint_as_float(r[j]), kz * reinterpret_cast<const float*>(&sm.cst[n >> 1])[n & 1]) * sm.mul[n];
+      if (dead || at >= sm.lim[n]) x = kNegInf;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(FULL, x, o));
+      if (lane == 0) sm.red[wg][w4][8 * k + j] = x;
+    }
+  }
+  group_sync(id);
+  if (w4 == 0 && lane < 8 * nch) {
+    const int n = 8 * (wg + kSoftGroups * (lane >> 3)) + (lane & 7);
+    float* neg = reinterpret_cast<float*>(&sm.cst[n >> 1]) + 2 + (n & 1);
+    const float m0 = -*neg;
+    const float m1 = fmaxf(fmaxf(sm.red[wg][0][lane], sm.red[wg][1][lane]), fmaxf(sm.red[wg][2][lane], sm.red[wg][3][lane]));
+    const bool raise = m1 > m0;
+    sm.alpha[n] = !raise ? 1.f : m0 == kUnset ? 0.f : exp2_fast(m0 - m1);
+    if (raise) *neg = -m1;
+  }
+  group_sync(id);
+  if (first) return;
+  tc::fence_after();
+#pragma unroll 1
+  for (int k = 0; k < nch; ++k) {
+    const int c0 = 8 * (wg + kSoftGroups * k);
+    uint32_t r[8];
+    tc::ld8(o_addr + c0, r);
+    tc::wait_ld(r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * sm.alpha[c0 + j]);
+    tc::st8(o_addr + c0, r);
+  }
+  tc::wait_st();
+}
+
 template <int D, int G, int QT>
 __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const DecodeArgs a) {
   using Gm = Geo<D>;
@@ -363,7 +432,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const DecodeA
   if (tid == 32) {
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(&sm.raw_full[i], 1);
-      mbar_init(&sm.raw_empty[i], 16);
+      mbar_init(&sm.raw_empty[i], 8);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.k_ready[i], 4);
@@ -398,202 +467,176 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const DecodeA
     while (walk.next(a, s)) {
       // the segment's queries, rotated, in log2 units: 8 rows a warp
       if (tid == 0) {
-        sm.edge[0] = 0x7fffffff;
-        sm.edge[1] = 0;
+        sm.edge = 0x7fffffff;
         sm.scaled = 0;
       }
-      asm volatile("barrier.cta.sync 3, 256;" ::: "memory");
-      for (int r = warp; r < kRB; r += kSoftWarps) {
-        const int b = s.bfirst + r / G;
-        const bool act = lane < D / 4;
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
+      soft_sync();
+      // all of a warp's loads are in flight before the first is used
+      constexpr int NR = kRB / kSoftWarps;
+      const bool act = lane < D / 4;
+      float x[NR][4];
+#pragma unroll
+      for (int k = 0; k < NR; ++k) {
+        const int r = warp + k * kSoftWarps;
+        x[k][0] = x[k][1] = x[k][2] = x[k][3] = 0.f;
         if (r < s.rows && act) {
-          const size_t q0 = (static_cast<size_t>(b) * a.Hq + static_cast<size_t>(s.g) * G + r % G) * D + 4 * lane;
+          const size_t q0 = (static_cast<size_t>(s.bfirst + r / G) * a.Hq + static_cast<size_t>(s.g) * G + r % G) * D + 4 * lane;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = load_q<QT>(a.q, q0 + e);
+          for (int e = 0; e < 4; ++e) x[k][e] = load_q<QT>(a.q, q0 + e);
         }
-        flip_signs4(x, lane, a.signs);
-        hadamard4(x, lane, a.h);
+      }
+#pragma unroll
+      for (int k = 0; k < NR; ++k) {
+        const int r = warp + k * kSoftWarps;
         float big = 0.f, sum = 0.f, f = 1.f;
+        if (r < s.rows) {
+          flip_signs4(x[k], lane, a.signs);
+          hadamard4(x[k], lane, a.h);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] *= a.qscale * kQShift / a.h;
-          big = fmaxf(big, fabsf(x[e]));
+          for (int e = 0; e < 4; ++e) {
+            x[k][e] *= a.qscale * kQShift / a.h;
+            big = fmaxf(big, fabsf(x[k][e]));
+          }
+#pragma unroll
+          for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(FULL, big, o));
+          if (big > 32768.f) {  // beyond fp16: down by a power of two (2^100 at most), undone on the logits
+            const int ex = min(((__float_as_int(big) >> 23) & 0xff) - 127 - 14, 100);
+            f = __int_as_float((127 + ex) << 23);
+            const float down = __int_as_float((127 - ex) << 23);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[k][e] *= down;
+          }
         }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(FULL, big, o));
-        if (big > 32768.f) {  // beyond fp16: down by a power of two (2^100 at most), undone on the logits
-          const int ex = min(((__float_as_int(big) >> 23) & 0xff) - 127 - 14, 100);
-          f = __int_as_float((127 + ex) << 23);
-          const float down = __int_as_float((127 - ex) << 23);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] *= down;
-        }
-#pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const __half hx = __float2half_rn(x[e]);
+          const __half hx = __float2half_rn(x[k][e]);
           sum += __half2float(hx);
-          const int k = key_order<D>(4 * lane + e);
-          if (act) sm.Q[(k >> 3) * (kRB * 8) + r * 8 + (k & 7)] = hx;
+          const int ko = key_order<D>(4 * lane + e);
+          if (act) sm.Q[(ko >> 3) * (kRB * 8) + r * 8 + (ko & 7)] = hx;
         }
+        if (r < s.rows) {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+          for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+        }
         if (lane == 0) {
           float* c = reinterpret_cast<float*>(&sm.cst[r >> 1]);
           c[r & 1] = sum * (1.f / kQShift);
           c[2 + (r & 1)] = r < s.rows ? -kUnset : 0.f;
-          reinterpret_cast<float*>(sm.mul)[r] = f;
-          const int lim = r < s.rows ? min(16 * s.grp.te, max(a.s, clamp_len(a.lens[b], cap) - a.w)) : 0;
-          sm.lim[r] = lim;
-          if (r < s.rows) {
-            atomicMin(&sm.edge[0], lim);
-            atomicMax(&sm.edge[1], lim);
-          }
+          sm.mul[r] = f;
           if (f != 1.f) sm.scaled = 1;
         }
       }
+      if (tid < kRB) {
+        const int lim = tid < s.rows ? min(16 * s.grp.te, max(a.s, clamp_len(a.lens[s.bfirst + tid / G], cap) - a.w)) : 0;
+        sm.lim[tid] = lim;
+        if (tid < s.rows) atomicMin(&sm.edge, lim);
+      }
       if (s.c == s.us) {
         const u32 last = (s.us + s.grp.tiles - 1) / sm.plan.Q;
-        for (int k = tid; k * G < s.rows; k += 256)
+        for (int k = tid; k * G < s.rows; k += kSoftThreads)
           a.pmeta[(s.bfirst + k) * a.Hkv + s.g] = make_uint4(s.slot, last - blockIdx.x + 1, k * G, 0u);
       }
       fence_proxy_async_smem();
-      asm volatile("barrier.cta.sync 3, 256;" ::: "memory");
+      soft_sync();
       warp_arrive(&sm.q_ready, lane);
-      const int lim_min = sm.edge[0], lim_max = sm.edge[1];
+      const int lim_min = sm.edge;
       const bool scaled = sm.scaled != 0;
-      const int ncol = min(32, max(0, ((s.rows + 15) & ~15) - 32 * wg));  // 0, 16 or 32
-      float l[32];
+      const int nch = (((s.rows + 15) >> 4) * 2 - wg + kSoftGroups - 1) / kSoftGroups;  // this group's chunks: 0, 1 or 2
+      uint64_t l2[8];  // this position's share of the rows' sums, two rows a register pair
 #pragma unroll
-      for (int j = 0; j < 32; ++j) l[j] = 0.f;
+      for (int j = 0; j < 8; ++j) l2[j] = 0ull;
 
       const u32 i0 = i;
+#pragma unroll 1
       for (u32 c = s.c; c < s.ce; ++c, ++i) {
-        const int t0 = s16 + static_cast<int>(c - s.us) * (kTile / 16);
-        const int st = static_cast<int>(i % kRaw), bf = static_cast<int>(i & 1);
-        wait(&sm.raw_full[st], i / kRaw);
-        const uint32_t kp = *reinterpret_cast<const uint32_t*>(sm.raw[st] + (pos >> 4) * Gm::T4B + 16 * D + 4 * (pos & 15));
-        const uint32_t vp = *reinterpret_cast<const uint32_t*>(sm.raw[st] + (pos >> 4) * Gm::T4B + 16 * D + 64 + 4 * (pos & 15));
-        const bool here = (sm.ok[st] >> (pos >> 4)) & 1u;
-        warp_arrive(&sm.raw_empty[st], lane);
-        // codes are c 2^-24 (rows 8-15 of a tile: 16 c 2^-24), queries times kQShift
-        const float ks = half_lo(kp) * ((pos & 8) ? 1048576.f / kQShift : 16777216.f / kQShift), kz = half_hi(kp);
-        const int at = 16 * t0 + pos;
-        const bool dead = !here || at < a.s;
-        const bool large = !dead && at < lim_max && value_large(vp);
-        const bool edge = 16 * t0 < a.s || 16 * t0 + kTile > lim_min || sm.ok[st] != 0xFFu;
+        const int p0 = 16 * (s16 + static_cast<int>(c - s.us) * (kTile / 16));
+        const int st = static_cast<int>(i % kRaw), bf = static_cast<int>(i & 1), at = p0 + pos;
         wait(&sm.qk_done[bf], i >> 1);
         tc::fence_after();
-
-        float e[32];
-        const uint64_t ks2 = tc::pack2(ks, ks), kz2 = tc::pack2(kz, kz);
-        // logits minus the running maximum (whole: the logits themselves)
-        auto logits = [&](bool minus) {
+        const float2 sz = sm.ksz[st][pos];
+        const uint32_t ok = sm.ok[st];
+        const uint4 lg = *reinterpret_cast<const uint4*>(sm.large[st]);
+        const uint32_t s_addr = tm + quad + C::S + kRB * bf;
+        const uint64_t ks2 = tc::pack2(sz.x, sz.x), kz2 = tc::pack2(sz.y, sz.y);
+        float e[16];  // logits minus the running maximum
+#pragma unroll 1
+        for (bool again = false;; again = true) {
+          uint32_t r[16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (16 * h >= ncol) break;
-            uint32_t sreg[16];
-            tc::ld16(tm + quad + C::S + kRB * bf + 32 * wg + 16 * h, sreg);
-            tc::wait_ld();
+          for (int k = 0; k < 2; ++k)
+            if (k < nch) tc::ld8(s_addr + 8 * (wg + kSoftGroups * k), r + 8 * k);
+          tc::wait_ld(r);
+          float top = kNegInf;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int n2 = 16 * wg + 8 * h + j;
-              const float4 cc = sm.cst[n2];
-              const uint64_t sv = tc::pack2(__uint_as_float(sreg[2 * j]), __uint_as_float(sreg[2 * j + 1]));
-              const uint64_t off = minus ? tc::pack2(cc.z, cc.w) : 0ull;
-              uint64_t x;
-              if (!scaled) {
-                x = tc::fma2(ks2, sv, tc::fma2(kz2, tc::pack2(cc.x, cc.y), off));
-              } else {
-                const float2 f = sm.mul[n2];
-                x = tc::fma2(tc::pack2(f.x, f.y), tc::fma2(ks2, sv, tc::mul2(kz2, tc::pack2(cc.x, cc.y))), off);
+          for (int k = 0; k < 2; ++k) {
+            if (k >= nch) break;
+            const float4* cst = &sm.cst[4 * (wg + kSoftGroups * k)];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float4 cc = cst[j];
+              const uint64_t sv = tc::pack2(__uint_as_float(r[8 * k + 2 * j]), __uint_as_float(r[8 * k + 2 * j + 1]));
+              const uint64_t x = tc::fma2(ks2, sv, tc::fma2(kz2, tc::pack2(cc.x, cc.y), tc::pack2(cc.z, cc.w)));
+              tc::unpack2(x, e[8 * k + 2 * j], e[8 * k + 2 * j + 1]);
+            }
+          }
+          if (scaled) {  // a row of the segment has its query scaled down
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              if (k >= nch) break;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const int n = 8 * (wg + kSoftGroups * k) + j;
+                const float* cc = reinterpret_cast<const float*>(&sm.cst[n >> 1]) + (n & 1);
+                e[8 * k + j] = fmaf(sm.mul[n], fmaf(sz.x, __uint_as_float(r[8 * k + j]), sz.y * cc[0]), cc[2]);
               }
-              tc::unpack2(x, e[16 * h + 2 * j], e[16 * h + 2 * j + 1]);
-              if (edge) {
-                if (dead || at >= sm.lim[2 * n2]) e[16 * h + 2 * j] = kNegInf;
-                if (dead || at >= sm.lim[2 * n2 + 1]) e[16 * h + 2 * j + 1] = kNegInf;
-              }
             }
           }
-        };
-        logits(true);
-        float top = kNegInf;
+          if (p0 < a.s || p0 + kTile > lim_min || ok != 0xFFu) {  // positions that some row does not attend
+            const bool dead = !((ok >> (pos >> 4)) & 1u) || at < a.s;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if ((j & ~15) < ncol) top = fmaxf(top, e[j]);
-        float lmul = 1.f;
-        if (ncol && group_or(id, top > kGrow || large)) {
-          const bool times16 = group_or(id, large);
-          // raise the running maxima to this unit's: column maxima over the 128 positions
-          logits(false);
-          float v[32];
+            for (int k = 0; k < 2; ++k) {
+              if (k >= nch) break;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = (j & ~15) < ncol ? e[j] : kNegInf;
-#pragma unroll
-          for (int o = 16; o; o >>= 1)
-#pragma unroll
-            for (int j = 0; j < o; ++j) {
-              const bool up = (lane & o) != 0;
-              const float got = __shfl_xor_sync(FULL, up ? v[j] : v[j + o], o);
-              v[j] = fmaxf(up ? v[j + o] : v[j], got);
+              for (int j = 0; j < 8; ++j)
+                if (dead || at >= sm.lim[8 * (wg + kSoftGroups * k) + j]) e[8 * k + j] = kNegInf;
             }
-          sm.red[wg][w4][lane] = v[0];
-          group_sync(id);
-          if (w4 == 0) {
-            const int n = 32 * wg + lane;
-            float* neg = reinterpret_cast<float*>(&sm.cst[n >> 1]) + 2 + (n & 1);
-            const float m0 = -*neg;
-            const float m1 = fmaxf(fmaxf(sm.red[wg][0][lane], sm.red[wg][1][lane]), fmaxf(sm.red[wg][2][lane], sm.red[wg][3][lane]));
-            const bool raise = lane < ncol && m1 > m0;
-            sm.alpha[n] = !raise ? 1.f : m0 == kUnset ? 0.f : exp2_fast(m0 - m1);
-            if (raise) *neg = -m1;
-          }
-          group_sync(id);
-          if (i > i0) {  // outputs so far: after the MMAs that are adding to them
-            wait(&sm.pv_done[(i - 1) & 1], (i - 1) >> 1);
-            tc::fence_after();
           }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (16 * h >= ncol) break;
-            uint32_t o[16];
-            const uint32_t addr = tm + quad + C::O + 32 * wg + 16 * h;
-            if (i > i0) {
-              tc::ld16(addr, o);
-              tc::wait_ld();
-            }
+          for (int k = 0; k < 2; ++k) {
+            if (k >= nch) break;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float al = sm.alpha[32 * wg + 16 * h + j];
-              l[16 * h + j] *= al;
-              o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
-            }
-            if (i > i0) tc::st16(addr, o);
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, e[8 * k + j]);
           }
-          tc::wait_st();
-          logits(true);
-          if (times16) {
-            lmul = 0.0625f;
+          if (again || !group_or(id, top > kGrow)) break;
+          if (i > i0) wait(&sm.pv_done[(i - 1) & 1], (i - 1) >> 1);
+          raise_maxima<D>(sm, wg, w4, lane, s_addr, tm + quad + C::O, nch, sz.x, sz.y, at, !((ok >> (pos >> 4)) & 1u) || at < a.s, i == i0);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if ((j & ~15) < ncol) e[j] += 4.f;
+          for (int k = 0; k < 2; ++k) {
+            if (k >= nch) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 al = *reinterpret_cast<const float2*>(&sm.alpha[8 * (wg + kSoftGroups * k) + 2 * j]);
+              l2[4 * k + j] = tc::mul2(l2[4 * k + j], tc::pack2(al.x, al.y));
+            }
           }
         }
         tc::fence_before();
         warp_arrive(&sm.s_free[bf], lane);
+        const bool times16 = (lg.x | lg.y | lg.z | lg.w) != 0u;
         if (i >= 2) wait(&sm.pv_done[bf], (i >> 1) - 1);  // the buffer's last product
+        __half* const pb = &sm.P[bf][wg * (kTile * 8) + pos * 8];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          if (8 * h >= ncol) break;
+        for (int k = 0; k < 2; ++k) {
+          if (k >= nch) break;
           uint32_t pk[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float p0 = exp2_fast(e[8 * h + 2 * j]), p1 = exp2_fast(e[8 * h + 2 * j + 1]);
-            l[8 * h + 2 * j] = fmaf(p0, lmul, l[8 * h + 2 * j]);
-            l[8 * h + 2 * j + 1] = fmaf(p1, lmul, l[8 * h + 2 * j + 1]);
-            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[j]) : "f"(p1), "f"(p0));
+            float x0 = exp2_fast(e[8 * k + 2 * j]), x1 = exp2_fast(e[8 * k + 2 * j + 1]);
+            l2[4 * k + j] = tc::add2(l2[4 * k + j], tc::pack2(x0, x1));
+            if (times16) x0 *= 16.f, x1 *= 16.f;
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[j]) : "f"(x1), "f"(x0));
           }
-          *reinterpret_cast<uint4*>(&sm.P[bf][(4 * wg + h) * (kTile * 8) + pos * 8]) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          *reinterpret_cast<uint4*>(pb + k * (kSoftGroups * kTile * 8)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
         fence_proxy_async_smem();
         tc::fence_before();
@@ -605,65 +648,75 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const DecodeA
       tc::fence_after();
       float* part = a.ppart + static_cast<size_t>(s.slot) * kRB * kPartRow<D>;
       const int dim = 32 * w4 + 4 * (lane & 7) + (lane >> 3);
+#pragma unroll 1
+      for (int k = 0; k < nch; ++k) {
+        const int c0 = 8 * (wg + kSoftGroups * k);
+        uint32_t o[8];
+        tc::ld8(tm + quad + C::O + c0, o);
+        tc::wait_ld(o);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (16 * h >= ncol) break;
-        uint32_t o[16];
-        tc::ld16(tm + quad + C::O + 32 * wg + 16 * h, o);
-        tc::wait_ld();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int n = 32 * wg + 16 * h + j;
-          if (n < s.rows && dim < D) part[n * kPartRow<D> + dim] = __uint_as_float(o[j]);
-        }
+        for (int j = 0; j < 8; ++j)
+          if (c0 + j < s.rows && dim < D) part[(c0 + j) * kPartRow<D> + dim] = __uint_as_float(o[j]);
       }
-      if (ncol) {
-        // sums over the 128 positions
+      // sums over the 128 positions: lanes j and j + 16 of each warp end with this group's column j
+      float l[16];
 #pragma unroll
-        for (int o = 16; o; o >>= 1)
+      for (int j = 0; j < 8; ++j) tc::unpack2(l2[j], l[2 * j], l[2 * j + 1]);
 #pragma unroll
-          for (int j = 0; j < o; ++j) {
-            const bool up = (lane & o) != 0;
-            const float got = __shfl_xor_sync(FULL, up ? l[j] : l[j + o], o);
-            l[j] = (up ? l[j + o] : l[j]) + got;
-          }
-        sm.red[wg][w4][lane] = l[0];
-        group_sync(id);
-        const int n = 32 * wg + lane;
-        if (w4 == 0 && n < s.rows) {
-          const float m = -(reinterpret_cast<const float*>(&sm.cst[n >> 1])[2 + (n & 1)]);
-          *reinterpret_cast<float2*>(part + n * kPartRow<D> + D) =
-              make_float2(m, (sm.red[wg][0][lane] + sm.red[wg][1][lane]) + (sm.red[wg][2][lane] + sm.red[wg][3][lane]));
+      for (int j = 0; j < 16; ++j) l[j] += __shfl_xor_sync(FULL, l[j], 16);
+#pragma unroll
+      for (int o = 8; o; o >>= 1)
+#pragma unroll
+        for (int j = 0; j < o; ++j) {
+          const bool up = (lane & o) != 0;
+          const float got = __shfl_xor_sync(FULL, up ? l[j] : l[j + o], o);
+          l[j] = (up ? l[j + o] : l[j]) + got;
         }
+      if (lane < 16) sm.red[wg][w4][lane] = l[0];
+      group_sync(id);
+      const int n = 8 * (wg + kSoftGroups * (lane >> 3)) + (lane & 7);
+      if (w4 == 0 && lane < 8 * nch && n < s.rows) {
+        const float m = -(reinterpret_cast<const float*>(&sm.cst[n >> 1])[2 + (n & 1)]);
+        *reinterpret_cast<float2*>(part + n * kPartRow<D> + D) =
+            make_float2(m, (sm.red[wg][0][lane] + sm.red[wg][1][lane]) + (sm.red[wg][2][lane] + sm.red[wg][3][lane]));
       }
       tc::fence_before();
-      asm volatile("barrier.cta.sync 3, 256;" ::: "memory");
+      soft_sync();
     }
   } else if (warp < kValWarp0) {
     // ------------------------------------------------------------------ keys
     const int w = warp - kKeyWarp0;
-    while (walk.next(a, s))
+    const int pos = 32 * w + lane;
+    // codes are c 2^-24 (rows 8-15 of a tile: 16 c 2^-24), queries times kQShift
+    const float unit = (pos & 8) ? 1048576.f / kQShift : 16777216.f / kQShift;
+    while (walk.next(a, s)) {
+      const int hi = attended_end<G>(a, s, cap, lane);
+#pragma unroll 1
       for (u32 c = s.c; c < s.ce; ++c, ++i) {
         const int st = static_cast<int>(i % kRaw), bf = static_cast<int>(i & 1);
+        const int at = 16 * (s16 + static_cast<int>(c - s.us) * (kTile / 16)) + pos;
         wait(&sm.raw_full[st], i / kRaw);
         if (i >= 2) wait(&sm.qk_done[bf], (i >> 1) - 1);
         tc::fence_after();
+        const uint8_t* tile = sm.raw[st] + (pos >> 4) * Gm::T4B + 16 * D + 4 * (pos & 15);
+        const uint32_t kp = *reinterpret_cast<const uint32_t*>(tile), vp = *reinterpret_cast<const uint32_t*>(tile + 64);
         unpack_keys<D>(sm.raw[st], tm + C::K + (D / 2) * bf, w, lane);
+        sm.ksz[st][pos] = make_float2(half_lo(kp) * unit, half_hi(kp));
+        const bool large = ((sm.ok[st] >> (pos >> 4)) & 1u) && at >= a.s && at < hi && value_large(vp);
+        const uint32_t any = __ballot_sync(FULL, large);
+        if (lane == 0) sm.large[st][w] = any;
         warp_arrive(&sm.raw_empty[st], lane);
         tc::wait_st();
         tc::fence_before();
         warp_arrive(&sm.k_ready[bf], lane);
       }
+    }
   } else if (warp < kCopyWarp) {
     // ------------------------------------------------------------------ values
     const int w = warp - kValWarp0;
     while (walk.next(a, s)) {
-      // positions that some row attends (others may be unwritten)
-      int hi = 0;
-      for (int r = lane; r * G < s.rows; r += 32) hi = max(hi, clamp_len(a.lens[s.bfirst + r], cap) - a.w);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) hi = max(hi, __shfl_xor_sync(FULL, hi, o));
-      hi = min(hi, 16 * s.grp.te);
+      const int hi = attended_end<G>(a, s, cap, lane);
+#pragma unroll 1
       for (u32 c = s.c; c < s.ce; ++c, ++i) {
         const int st = static_cast<int>(i % kRaw), bf = static_cast<int>(i & 1);
         const int p0 = 16 * (s16 + static_cast<int>(c - s.us) * (kTile / 16));
@@ -726,7 +779,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const DecodeA
   } else {
     // ------------------------------------------------------------------ matrix products
     if (lane == 0) {
-      const uint32_t q0 = smem_u32(sm.Q), p0 = smem_u32(sm.P);
+      // the descriptors' low bits are the address in units of 16 bytes: steps are added to them
+      const uint64_t q_desc = tc::smem_desc(smem_u32(sm.Q), kRB * 16, 128), p_desc = tc::smem_desc(smem_u32(sm.P), 128, kTile * 16);
       u32 seg = 0, first = 0;
       uint32_t nmma = 0;
       auto pv = [&](u32 k, bool acc) {  // products of unit k
@@ -736,10 +790,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const DecodeA
         tc::fence_after();
         if (!*abort) {
           const uint32_t id = tc::idesc_f16(kTile, nmma, true);
+          const uint64_t b = p_desc + bf * (kRB * kTile * 2 / 16);
+          const uint32_t av = tm + C::V + (kTile / 2) * bf;
 #pragma unroll
-          for (int x = 0; x < kTile / 16; ++x)
-            tc::mma_ts(tm + C::O, tm + C::V + (kTile / 2) * bf + 8 * x, tc::smem_desc(p0 + bf * (kRB * kTile * 2) + x * 256, 128, kTile * 16), id,
-                       acc || x > 0);
+          for (int x = 0; x < kTile / 16; ++x) tc::mma_ts(tm + C::O, av + 8 * x, b + x * (256 / 16), id, acc || x > 0);
         }
         tc::commit(&sm.pv_done[bf]);
       };
@@ -754,9 +808,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const DecodeA
           if (i >= 2) wait(&sm.s_free[bf], (i >> 1) - 1);
           tc::fence_after();
           if (!*abort) {
+            const uint32_t ak = tm + C::K + (D / 2) * bf, ds = tm + C::S + kRB * bf;
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x)
-              tc::mma_ts(tm + C::S + kRB * bf, tm + C::K + (D / 2) * bf + 8 * x, tc::smem_desc(q0 + x * (2 * kRB * 16), kRB * 16, 128), id, x > 0);
+            for (int x = 0; x < D / 16; ++x) tc::mma_ts(ds, ak + 8 * x, q_desc + x * (2 * kRB * 16 / 16), id, x > 0);
           }
           tc::commit(&sm.qk_done[bf]);
           if (i > first) pv(i - 1, i - 1 > first);
