@@ -28,6 +28,10 @@ constexpr int kRB = 64;          // query rows of a prefix segment: the MMA's co
 constexpr int kTile = 128;       // positions of a prefix unit: the MMA's rows
 constexpr int kRaw = 4;          // buffers of packed tiles
 
+// The loops' rare branches: their code goes out of the way of the straight path, whose instruction
+// fetch a taken branch would interrupt.
+__device__ __forceinline__ bool unlikely(bool x) { return __builtin_expect(x, 0); }
+
 // ------------------------------------------------------------------ the prefix schedule
 //
 // Groups of consecutive batch rows share the pages of their prefix.  A segment is (group, KV head,
@@ -155,6 +159,18 @@ constexpr float kUnset = -1e30f;   // running maximum of a row that has seen no 
 constexpr float kGrow = 8.f;       // a logit this far above the running maximum raises it
 constexpr float kQShift = 64.f;    // queries enter fp16 times this: typical ones are then near one
 
+// The units of this thread block, segment by segment: every warp walks them on its own.  The state
+// lives in shared memory (it is read once a segment; the loops over units need the registers).
+struct Segment {
+  u32 at, end, unit0, seg0;  // next and last unit of the block; first unit and segment of group gr
+  int gr;
+  int te, b0;                // the group's prefix end (16-position tiles) and first row
+  int g, rows, bfirst;       // KV head, query rows, first sequence
+  int p0;                    // first position
+  u32 n;                     // units
+  u32 slot, blocks;          // partial index; thread blocks from this one on (0: not the segment's first)
+};
+
 template <int D>
 struct SmemPrefix {
   uint8_t raw[kRaw][8 * Geo<D>::T4B];
@@ -177,6 +193,7 @@ struct SmemPrefix {
   uint32_t tmem;
   int abort;
   Plan plan;
+  Segment seg[kPrefixThreads / 32];
 };
 
 // TMEM columns: keys and values as A operands (two fp16 a column), scores, outputs.
@@ -186,21 +203,26 @@ struct Cols {
   static_assert(O + kRB <= All, "TMEM columns");
 };
 
+// The same value in every lane, known as such to the compiler: branches on it need no reconvergence.
+template <typename T>
+__device__ __forceinline__ T uniform(T x) { return __shfl_sync(FULL, x, 0); }
+
 // A bounded wait that gives up when any warp of the block has: every role then runs its loop to the
-// end without waiting, so that all of them reach the end of the kernel.  Short, because every role
-// has copies of it and they all run from one instruction cache; the clock is read every 64 polls.
+// end without waiting, so that all of them reach the end of the kernel.
 __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err, uint64_t limit_ns) {
-  uint64_t t0 = 0;
+  if (unlikely(!mbar_try_wait(bar, parity))) {
+    uint64_t t0 = 0;
 #pragma unroll 1
-  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
-    if (it & 63u) continue;
-    const uint64_t t = global_timer_ns();
-    if (t0 == 0) t0 = t;
-    if (*abort) return;
-    if (t - t0 > limit_ns || it >= kWaitLimitPolls) {
-      *abort = 1;
-      atomicOr(err, KV4_DEVERR_WAIT_LIMIT);
-      return;
+    for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+      if (it & 63u) continue;
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      if (*abort) return;
+      if (t - t0 > limit_ns || it >= kWaitLimitPolls) {
+        *abort = 1;
+        atomicOr(err, KV4_DEVERR_WAIT_LIMIT);
+        return;
+      }
     }
   }
 }
@@ -225,45 +247,56 @@ __device__ __forceinline__ bool group_or(int id, bool x) {
 __device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 5, %0;" ::"n"(kSoftThreads) : "memory"); }
 __device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
 
-// The units of this thread block, segment by segment: every role walks them on its own.
-struct Segment {
-  Group grp;
-  int g, rb, rows, bfirst;
-  u32 us, c, ce;      // first unit of the segment, this block's range of it
-  u32 slot;           // partial index
-};
-template <int G>
-struct Walk {
-  u32 c, c1, unit0, seg0;
-  int gr;
-  __device__ explicit Walk(const Plan& p) : c(blockIdx.x * p.Q), c1(min(blockIdx.x * p.Q + p.Q, p.total)), unit0(p.unit0), seg0(p.seg0), gr(p.group) {}
-  __device__ bool next(const DecodeArgs& a, Segment& s) {
-    while (c < c1) {
-      bool bad;
-      s.grp = load_group<G>(a, gr, &bad);
-      const u32 nseg = static_cast<u32>(a.Hkv) * s.grp.nrb;
-      if (s.grp.tiles == 0 || c >= unit0 + nseg * s.grp.tiles) {
-        if (s.grp.tiles) {
-          unit0 += nseg * s.grp.tiles;
-          seg0 += nseg;
-        }
-        ++gr;
-        continue;
-      }
-      const u32 sg = (c - unit0) / s.grp.tiles;
-      s.us = unit0 + sg * s.grp.tiles;
-      s.g = static_cast<int>(sg / s.grp.nrb);
-      s.rb = static_cast<int>(sg % s.grp.nrb);
-      s.rows = min(kRB, s.grp.n * G - s.rb * kRB);
-      s.bfirst = s.grp.b0 + s.rb * (kRB / G);
-      s.c = c;
-      s.ce = c = min(c1, s.us + s.grp.tiles);
-      s.slot = blockIdx.x + seg0 + sg;
-      return true;
-    }
-    return false;
+__device__ __forceinline__ void walk_start(Segment& s, const Plan& p, int lane) {
+  if (lane == 0) {
+    s.at = blockIdx.x * p.Q;
+    s.end = min(blockIdx.x * p.Q + p.Q, p.total);
+    s.unit0 = p.unit0;
+    s.seg0 = p.seg0;
+    s.gr = p.group;
   }
-};
+  __syncwarp();
+}
+
+template <int G>
+__device__ __noinline__ bool walk_next(const DecodeArgs& a, const Plan& p, Segment& s, int lane) {
+  u32 c = s.at, unit0 = s.unit0, seg0 = s.seg0;
+  int gr = s.gr;
+  __syncwarp();
+  while (c < s.end) {
+    bool bad;
+    const Group grp = load_group<G>(a, gr, &bad);
+    const u32 nseg = static_cast<u32>(a.Hkv) * grp.nrb;
+    if (grp.tiles == 0 || c >= unit0 + nseg * grp.tiles) {
+      if (grp.tiles) {
+        unit0 += nseg * grp.tiles;
+        seg0 += nseg;
+      }
+      ++gr;
+      continue;
+    }
+    const u32 sg = (c - unit0) / grp.tiles, us = unit0 + sg * grp.tiles, ce = min(s.end, us + grp.tiles);
+    const int rb = static_cast<int>(sg % grp.nrb);
+    if (lane == 0) {
+      s.at = ce;
+      s.unit0 = unit0;
+      s.seg0 = seg0;
+      s.gr = gr;
+      s.te = grp.te;
+      s.b0 = grp.b0;
+      s.g = static_cast<int>(sg / grp.nrb);
+      s.rows = min(kRB, grp.n * G - rb * kRB);
+      s.bfirst = grp.b0 + rb * (kRB / G);
+      s.p0 = 16 * (a.s >> 4) + static_cast<int>(c - us) * kTile;
+      s.n = ce - c;
+      s.slot = blockIdx.x + seg0 + sg;
+      s.blocks = c == us ? (us + grp.tiles - 1) / p.Q - blockIdx.x + 1 : 0;
+    }
+    __syncwarp();
+    return true;
+  }
+  return false;
+}
 
 // End of the positions that some row of the segment attends; those past it may be unwritten.
 template <int G>
@@ -272,7 +305,7 @@ __device__ __forceinline__ int attended_end(const DecodeArgs& a, const Segment& 
   for (int r = lane; r * G < s.rows; r += 32) hi = max(hi, clamp_len(a.lens[s.bfirst + r], cap) - a.w);
 #pragma unroll
   for (int o = 16; o; o >>= 1) hi = max(hi, __shfl_xor_sync(FULL, hi, o));
-  return min(hi, 16 * s.grp.te);
+  return min(hi, 16 * s.te);
 }
 
 // Row of the A operand's k order that dimension d takes (the order in which unpack_keys meets it).
@@ -327,7 +360,7 @@ __device__ __forceinline__ void unpack_values(const uint8_t* raw, uint32_t tmem,
   const int a = lane >> 2, q = lane & 3, Q = 8 * w + a;
   const uint8_t* vw = raw + 8 * D + ((Q / Gm::WPC) * 4 + q) * Gm::CH + 4 * (Q % Gm::WPC);
   const uint8_t* pp = raw + 16 * D + 64 + 8 * q;
-  const bool whole = ok == 0xFFu && lo <= 0 && hi >= kTile;
+  const bool part = ok != 0xFFu || lo > 0 || hi < kTile;
   const __half2 sixteenth = __float2half2_rn(0.0625f);
   // the unit's instructions are few: the warps of all roles run from one instruction cache
 #pragma unroll 1
@@ -338,14 +371,14 @@ __device__ __forceinline__ void unpack_values(const uint8_t* raw, uint32_t tmem,
       const int T = 4 * blk + (i >> 1), half = i & 1;
       const uint32_t x = *reinterpret_cast<const uint32_t*>(vw + T * Gm::T4B + half * 32 * Gm::CH);
       uint2 sz = *reinterpret_cast<const uint2*>(pp + T * Gm::T4B + half * 32);
-      if (!whole) {
+      if (unlikely(part)) {
         const int p0 = 16 * T + 8 * half + 2 * q, h = ((ok >> T) & 1u) ? hi : 0;
         if (p0 < lo || p0 >= h) sz.x = 0u;
         if (p0 + 1 < lo || p0 + 1 >= h) sz.y = 0u;
       }
       const uint32_t s2 = prmt(sz.x, sz.y, 0x5410u), z2 = prmt(sz.x, sz.y, 0x7632u);
       __half2 s = *reinterpret_cast<const __half2*>(&s2), z = *reinterpret_cast<const __half2*>(&z2);
-      if (large) {
+      if (unlikely(large)) {
         s = __hmul2(s, sixteenth);
         z = __hmul2(z, sixteenth);
       }
@@ -368,63 +401,123 @@ __device__ __forceinline__ void unpack_values(const uint8_t* raw, uint32_t tmem,
   }
 }
 
-// Raise the running maxima of softmax group wg's columns (nch chunks of 8) to this unit's: column
-// maxima over the 128 positions of its threads, factors for what was summed so far to sm.alpha
-// (outputs in TMEM are rescaled here, after the MMAs that are adding to them).  Seldom taken, kept
-// out of the loop.  s_addr, o_addr: scores and outputs of this warp's TMEM lanes.
+// What a softmax warp needs to find its unit.
+struct SoftUnit {
+  uint32_t s_addr, o_addr;  // scores and outputs of this warp's TMEM lanes
+  int wg, w4, lane, nch;    // softmax group, warp in it, lane, the group's 8-column chunks
+  int st, bf, p0;           // buffers, first position of the unit
+  bool first, raise;        // first unit of the segment; the running maxima have to be raised
+};
+
+// A unit off the straight path, for one warp of a softmax group (all four take it together): positions
+// that some row does not attend, scaled queries, values taken times 1/16, and running maxima to be
+// raised (outputs in TMEM are rescaled, after the MMAs that are adding to them).  Reads the scores,
+// leaves the probabilities in the P buffer and the positions' sums in l.  Kept out of the loop: the
+// loops of all roles share the instruction cache, and this one needs no registers there.
 template <int D>
-__device__ __noinline__ void raise_maxima(SmemPrefix<D>& sm, int wg, int w4, int lane, uint32_t s_addr, uint32_t o_addr, int nch, float ks,
-                                          float kz, int at, bool dead, bool first) {
-  const int id = 1 + wg;
+__device__ __noinline__ void soft_unit_slow(SmemPrefix<D>& sm, const SoftUnit u, int sinks, u32 i, float* l, uint32_t* err, uint64_t limit_ns) {
+  const int pos = 32 * u.w4 + u.lane, at = u.p0 + pos, id = 1 + u.wg;
+  const float2 sz = sm.ksz[u.st][pos];
+  const uint32_t ok = sm.ok[u.st];
+  const bool dead = !((ok >> (pos >> 4)) & 1u) || at < sinks;
+  const bool large = (sm.large[u.st][0] | sm.large[u.st][1] | sm.large[u.st][2] | sm.large[u.st][3]) != 0u;
+  auto logit = [&](int n, uint32_t s) {
+    const float x = sm.mul[n] * fmaf(sz.x, __uint_as_float(s), sz.y * reinterpret_cast<const float*>(&sm.cst[n >> 1])[n & 1]);
+    return dead || at >= sm.lim[n] ? kNegInf : x;
+  };
+  auto neg_max = [&](int n) -> float& { return reinterpret_cast<float*>(&sm.cst[n >> 1])[2 + (n & 1)]; };
+  bool raise = u.raise;
+  if (!raise) {
+    float top = kNegInf;
 #pragma unroll 1
-  for (int k = 0; k < nch; ++k) {
-    const int c0 = 8 * (wg + kSoftGroups * k);
-    uint32_t r[8];
-    tc::ld8(s_addr + c0, r);
-    tc::wait_ld(r);
+    for (int k = 0; k < u.nch; ++k) {
+      const int c0 = 8 * (u.wg + kSoftGroups * k);
+      uint32_t r[8];
+      tc::ld8(u.s_addr + c0, r);
+      tc::wait_ld(r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int n = c0 + j;
-      float x = fmaf(ks, __uint_as_float(r[j]), kz * reinterpret_cast<const float*>(&sm.cst[n >> 1])[n & 1]) * sm.mul[n];
-      if (dead || at >= sm.lim[n]) x = kNegInf;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(FULL, x, o));
-      if (lane == 0) sm.red[wg][w4][8 * k + j] = x;
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, logit(c0 + j, r[j]) + neg_max(c0 + j));
     }
+    raise = group_or(id, top > kGrow);
   }
-  group_sync(id);
-  if (w4 == 0 && lane < 8 * nch) {
-    const int n = 8 * (wg + kSoftGroups * (lane >> 3)) + (lane & 7);
-    float* neg = reinterpret_cast<float*>(&sm.cst[n >> 1]) + 2 + (n & 1);
-    const float m0 = -*neg;
-    const float m1 = fmaxf(fmaxf(sm.red[wg][0][lane], sm.red[wg][1][lane]), fmaxf(sm.red[wg][2][lane], sm.red[wg][3][lane]));
-    const bool raise = m1 > m0;
-    sm.alpha[n] = !raise ? 1.f : m0 == kUnset ? 0.f : exp2_fast(m0 - m1);
-    if (raise) *neg = -m1;
-  }
-  group_sync(id);
-  if (first) return;
-  tc::fence_after();
+  if (raise) {
+    // column maxima over the 128 positions
 #pragma unroll 1
-  for (int k = 0; k < nch; ++k) {
-    const int c0 = 8 * (wg + kSoftGroups * k);
-    uint32_t r[8];
-    tc::ld8(o_addr + c0, r);
+    for (int k = 0; k < u.nch; ++k) {
+      const int c0 = 8 * (u.wg + kSoftGroups * k);
+      uint32_t r[8];
+      tc::ld8(u.s_addr + c0, r);
+      tc::wait_ld(r);
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = logit(c0 + j, r[j]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = fmaxf(x[j], __shfl_xor_sync(FULL, x[j], o));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (u.lane == j) sm.red[u.wg][u.w4][8 * k + j] = x[j];
+    }
+    group_sync(id);
+    if (u.w4 == 0 && u.lane < 8 * u.nch) {
+      const int n = 8 * (u.wg + kSoftGroups * (u.lane >> 3)) + (u.lane & 7);
+      const float m0 = -neg_max(n);
+      const float m1 = fmaxf(fmaxf(sm.red[u.wg][0][u.lane], sm.red[u.wg][1][u.lane]), fmaxf(sm.red[u.wg][2][u.lane], sm.red[u.wg][3][u.lane]));
+      const bool up = m1 > m0;
+      sm.alpha[n] = !up ? 1.f : m0 == kUnset ? 0.f : exp2_fast(m0 - m1);
+      if (up) neg_max(n) = -m1;
+    }
+    group_sync(id);
+    if (!u.first) {
+      wait_bar(&sm.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1u, &sm.abort, err, limit_ns);
+      tc::fence_after();
+    }
+#pragma unroll 1
+    for (int k = 0; k < u.nch; ++k) {
+      const int c0 = 8 * (u.wg + kSoftGroups * k);
+      uint32_t r[8];
+      if (!u.first) {
+        tc::ld8(u.o_addr + c0, r);
+        tc::wait_ld(r);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        l[8 * k + j] *= sm.alpha[c0 + j];
+        if (!u.first) r[j] = __float_as_uint(__uint_as_float(r[j]) * sm.alpha[c0 + j]);
+      }
+      if (!u.first) tc::st8(u.o_addr + c0, r);
+    }
+    tc::wait_st();
+  }
+  if (i >= 2) wait_bar(&sm.pv_done[u.bf], ((i >> 1) - 1) & 1u, &sm.abort, err, limit_ns);  // the buffer's last product
+#pragma unroll 1
+  for (int k = 0; k < u.nch; ++k) {
+    const int c0 = 8 * (u.wg + kSoftGroups * k);
+    uint32_t r[8], pk[4];
+    tc::ld8(u.s_addr + c0, r);
     tc::wait_ld(r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * sm.alpha[c0 + j]);
-    tc::st8(o_addr + c0, r);
+    for (int j = 0; j < 4; ++j) {
+      const float x0 = exp2_fast(logit(c0 + 2 * j, r[2 * j]) + neg_max(c0 + 2 * j));
+      const float x1 = exp2_fast(logit(c0 + 2 * j + 1, r[2 * j + 1]) + neg_max(c0 + 2 * j + 1));
+      l[8 * k + 2 * j] += x0;
+      l[8 * k + 2 * j + 1] += x1;
+      __half2 t = __floats2half2_rn(x0, x1);
+      if (large) t = __hmul2(t, __float2half2_rn(16.f));  // the unit's values were taken times 1/16
+      pk[j] = *reinterpret_cast<const uint32_t*>(&t);
+    }
+    *reinterpret_cast<uint4*>(&sm.P[u.bf][c0 * kTile + pos * 8]) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
   }
-  tc::wait_st();
 }
 
 template <int D, int G, int QT>
-__global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_constant__ DecodeArgs a) {
   using Gm = Geo<D>;
   using C = Cols<D>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   SmemPrefix<D>& sm = *reinterpret_cast<SmemPrefix<D>*>(smem_raw);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   const int cap = a.stride * a.P;
   volatile int* abort = &sm.abort;
   pdl_wait();
@@ -451,20 +544,19 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const DecodeA
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tm = sm.tmem;
+  const uint32_t tm = uniform(sm.tmem);
   auto wait = [&](uint64_t* bar, u32 n) { wait_bar(bar, n & 1u, abort, a.err, a.wait_ns); };  // the n-th completion (0-based)
 
-  Walk<G> walk(sm.plan);
-  Segment s;
+  Segment& s = sm.seg[warp];
+  walk_start(s, sm.plan, lane);
   u32 i = 0;  // units so far
-  const int s16 = a.s >> 4;
 
   if (warp < kSoftWarps) {
     // ------------------------------------------------------------------ softmax
     const int wg = warp >> 2, w4 = warp & 3, pos = 32 * w4 + lane, id = 1 + wg;
     const uint32_t quad = static_cast<uint32_t>(32 * w4) << 16;
     if (a.stall_test) wait(&sm.stall, 0);
-    while (walk.next(a, s)) {
+    while (walk_next<G>(a, sm.plan, s, lane)) {
       // the segment's queries, rotated, in log2 units: 8 rows a warp
       if (tid == 0) {
         sm.edge = 0x7fffffff;
@@ -527,40 +619,36 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const DecodeA
         }
       }
       if (tid < kRB) {
-        const int lim = tid < s.rows ? min(16 * s.grp.te, max(a.s, clamp_len(a.lens[s.bfirst + tid / G], cap) - a.w)) : 0;
+        const int lim = tid < s.rows ? min(16 * s.te, max(a.s, clamp_len(a.lens[s.bfirst + tid / G], cap) - a.w)) : 0;
         sm.lim[tid] = lim;
         if (tid < s.rows) atomicMin(&sm.edge, lim);
       }
-      if (s.c == s.us) {
-        const u32 last = (s.us + s.grp.tiles - 1) / sm.plan.Q;
-        for (int k = tid; k * G < s.rows; k += kSoftThreads)
-          a.pmeta[(s.bfirst + k) * a.Hkv + s.g] = make_uint4(s.slot, last - blockIdx.x + 1, k * G, 0u);
-      }
+      if (s.blocks)
+        for (int k = tid; k * G < s.rows; k += kSoftThreads) a.pmeta[(s.bfirst + k) * a.Hkv + s.g] = make_uint4(s.slot, s.blocks, k * G, 0u);
       fence_proxy_async_smem();
       soft_sync();
       warp_arrive(&sm.q_ready, lane);
-      const int lim_min = sm.edge;
-      const bool scaled = sm.scaled != 0;
-      const int nch = (((s.rows + 15) >> 4) * 2 - wg + kSoftGroups - 1) / kSoftGroups;  // this group's chunks: 0, 1 or 2
+      // a scaled query takes every unit of the segment off the straight path, a row block without rows none
+      const int lim_min = uniform(sm.scaled ? -1 : sm.edge), sinks = a.s;
+      const int nch = uniform((((s.rows + 15) >> 4) * 2 - wg + kSoftGroups - 1) / kSoftGroups);  // this group's chunks: 0, 1 or 2
       uint64_t l2[8];  // this position's share of the rows' sums, two rows a register pair
 #pragma unroll
       for (int j = 0; j < 8; ++j) l2[j] = 0ull;
 
-      const u32 i0 = i;
+      const u32 i0 = i, i1 = i + uniform(s.n);
 #pragma unroll 1
-      for (u32 c = s.c; c < s.ce; ++c, ++i) {
-        const int p0 = 16 * (s16 + static_cast<int>(c - s.us) * (kTile / 16));
-        const int st = static_cast<int>(i % kRaw), bf = static_cast<int>(i & 1), at = p0 + pos;
+      for (int p0 = uniform(s.p0); i != i1; ++i, p0 += kTile) {
+        const int st = static_cast<int>(i % kRaw), bf = static_cast<int>(i & 1);
         wait(&sm.qk_done[bf], i >> 1);
         tc::fence_after();
-        const float2 sz = sm.ksz[st][pos];
-        const uint32_t ok = sm.ok[st];
-        const uint4 lg = *reinterpret_cast<const uint4*>(sm.large[st]);
         const uint32_t s_addr = tm + quad + C::S + kRB * bf;
-        const uint64_t ks2 = tc::pack2(sz.x, sz.x), kz2 = tc::pack2(sz.y, sz.y);
-        float e[16];  // logits minus the running maximum
-#pragma unroll 1
-        for (bool again = false;; again = true) {
+        // off the straight path: positions that some row does not attend, scaled queries, large values
+        const uint4 lg = *reinterpret_cast<const uint4*>(sm.large[st]);
+        bool slow = uniform(lg.x | lg.y | lg.z | lg.w | (sm.ok[st] ^ 0xFFu)) != 0u || p0 < sinks || p0 + kTile > lim_min;
+        uint32_t pk[8];
+        if (!slow) {
+          const float2 sz = sm.ksz[st][pos];
+          const uint64_t ks2 = tc::pack2(sz.x, sz.x), kz2 = tc::pack2(sz.y, sz.y);
           uint32_t r[16];
 #pragma unroll
           for (int k = 0; k < 2; ++k)
@@ -572,71 +660,48 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const DecodeA
             if (k >= nch) break;
             const float4* cst = &sm.cst[4 * (wg + kSoftGroups * k)];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float4 cc = cst[j];
-              const uint64_t sv = tc::pack2(__uint_as_float(r[8 * k + 2 * j]), __uint_as_float(r[8 * k + 2 * j + 1]));
+            for (int j = 4 * k; j < 4 * k + 4; ++j) {  // logits minus the running maximum
+              const float4 cc = cst[j - 4 * k];
+              const uint64_t sv = tc::pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
               const uint64_t x = tc::fma2(ks2, sv, tc::fma2(kz2, tc::pack2(cc.x, cc.y), tc::pack2(cc.z, cc.w)));
-              tc::unpack2(x, e[8 * k + 2 * j], e[8 * k + 2 * j + 1]);
+              float e0, e1;
+              tc::unpack2(x, e0, e1);
+              r[2 * j] = __float_as_uint(e0);
+              r[2 * j + 1] = __float_as_uint(e1);
+              top = tc::max3(top, e0, e1);
             }
           }
-          if (scaled) {  // a row of the segment has its query scaled down
+          slow = uniform(static_cast<int>(group_or(id, top > kGrow))) != 0;
+          if (!slow) {
+            tc::fence_before();
+            warp_arrive(&sm.s_free[bf], lane);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               if (k >= nch) break;
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const int n = 8 * (wg + kSoftGroups * k) + j;
-                const float* cc = reinterpret_cast<const float*>(&sm.cst[n >> 1]) + (n & 1);
-                e[8 * k + j] = fmaf(sm.mul[n], fmaf(sz.x, __uint_as_float(r[8 * k + j]), sz.y * cc[0]), cc[2]);
+              for (int j = 4 * k; j < 4 * k + 4; ++j) {
+                const float x0 = exp2_fast(__uint_as_float(r[2 * j])), x1 = exp2_fast(__uint_as_float(r[2 * j + 1]));
+                l2[j] = tc::add2(l2[j], tc::pack2(x0, x1));
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[j]) : "f"(x1), "f"(x0));
               }
             }
-          }
-          if (p0 < a.s || p0 + kTile > lim_min || ok != 0xFFu) {  // positions that some row does not attend
-            const bool dead = !((ok >> (pos >> 4)) & 1u) || at < a.s;
+            if (i >= 2) wait(&sm.pv_done[bf], (i >> 1) - 1);  // the buffer's last product
+            __half* const pb = &sm.P[bf][wg * (kTile * 8) + pos * 8];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              if (k >= nch) break;
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (dead || at >= sm.lim[8 * (wg + kSoftGroups * k) + j]) e[8 * k + j] = kNegInf;
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (k >= nch) break;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, e[8 * k + j]);
-          }
-          if (again || !group_or(id, top > kGrow)) break;
-          if (i > i0) wait(&sm.pv_done[(i - 1) & 1], (i - 1) >> 1);
-          raise_maxima<D>(sm, wg, w4, lane, s_addr, tm + quad + C::O, nch, sz.x, sz.y, at, !((ok >> (pos >> 4)) & 1u) || at < a.s, i == i0);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (k >= nch) break;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 al = *reinterpret_cast<const float2*>(&sm.alpha[8 * (wg + kSoftGroups * k) + 2 * j]);
-              l2[4 * k + j] = tc::mul2(l2[4 * k + j], tc::pack2(al.x, al.y));
-            }
+            for (int k = 0; k < 2; ++k)
+              if (k < nch) *reinterpret_cast<uint4*>(pb + k * (kSoftGroups * kTile * 8)) = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
           }
         }
-        tc::fence_before();
-        warp_arrive(&sm.s_free[bf], lane);
-        const bool times16 = (lg.x | lg.y | lg.z | lg.w) != 0u;
-        if (i >= 2) wait(&sm.pv_done[bf], (i >> 1) - 1);  // the buffer's last product
-        __half* const pb = &sm.P[bf][wg * (kTile * 8) + pos * 8];
+        if (unlikely(slow)) {
+          float l[16];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if (k >= nch) break;
-          uint32_t pk[4];
+          for (int j = 0; j < 8; ++j) tc::unpack2(l2[j], l[2 * j], l[2 * j + 1]);
+          const bool voted = uniform(lg.x | lg.y | lg.z | lg.w | (sm.ok[st] ^ 0xFFu)) == 0u && p0 >= sinks && p0 + kTile <= lim_min;
+          soft_unit_slow<D>(sm, SoftUnit{s_addr, tm + quad + C::O, wg, w4, lane, nch, st, bf, p0, i == i0, voted || i == i0}, a.s, i, l, a.err, a.wait_ns);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float x0 = exp2_fast(e[8 * k + 2 * j]), x1 = exp2_fast(e[8 * k + 2 * j + 1]);
-            l2[4 * k + j] = tc::add2(l2[4 * k + j], tc::pack2(x0, x1));
-            if (times16) x0 *= 16.f, x1 *= 16.f;
-            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[j]) : "f"(x1), "f"(x0));
-          }
-          *reinterpret_cast<uint4*>(pb + k * (kSoftGroups * kTile * 8)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          for (int j = 0; j < 8; ++j) l2[j] = tc::pack2(l[2 * j], l[2 * j + 1]);
+          tc::fence_before();
+          warp_arrive(&sm.s_free[bf], lane);
         }
         fence_proxy_async_smem();
         tc::fence_before();
@@ -689,12 +754,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const DecodeA
     const int pos = 32 * w + lane;
     // codes are c 2^-24 (rows 8-15 of a tile: 16 c 2^-24), queries times kQShift
     const float unit = (pos & 8) ? 1048576.f / kQShift : 16777216.f / kQShift;
-    while (walk.next(a, s)) {
+    while (walk_next<G>(a, sm.plan, s, lane)) {
       const int hi = attended_end<G>(a, s, cap, lane);
+      const u32 i1 = i + uniform(s.n);
 #pragma unroll 1
-      for (u32 c = s.c; c < s.ce; ++c, ++i) {
+      for (int at = uniform(s.p0) + pos; i != i1; ++i, at += kTile) {
         const int st = static_cast<int>(i % kRaw), bf = static_cast<int>(i & 1);
-        const int at = 16 * (s16 + static_cast<int>(c - s.us) * (kTile / 16)) + pos;
         wait(&sm.raw_full[st], i / kRaw);
         if (i >= 2) wait(&sm.qk_done[bf], (i >> 1) - 1);
         tc::fence_after();
@@ -714,16 +779,16 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const DecodeA
   } else if (warp < kCopyWarp) {
     // ------------------------------------------------------------------ values
     const int w = warp - kValWarp0;
-    while (walk.next(a, s)) {
+    while (walk_next<G>(a, sm.plan, s, lane)) {
       const int hi = attended_end<G>(a, s, cap, lane);
+      const u32 i1 = i + uniform(s.n);
 #pragma unroll 1
-      for (u32 c = s.c; c < s.ce; ++c, ++i) {
+      for (int p0 = uniform(s.p0); i != i1; ++i, p0 += kTile) {
         const int st = static_cast<int>(i % kRaw), bf = static_cast<int>(i & 1);
-        const int p0 = 16 * (s16 + static_cast<int>(c - s.us) * (kTile / 16));
         wait(&sm.raw_full[st], i / kRaw);
         if (i >= 2) wait(&sm.pv_done[bf], (i >> 1) - 1);
         tc::fence_after();
-        const uint32_t ok = sm.ok[st];
+        const uint32_t ok = uniform(sm.ok[st]);
         if (32 * w < D) {
           const uint4 vp = *reinterpret_cast<const uint4*>(sm.raw[st] + (lane >> 2) * Gm::T4B + 16 * D + 64 + 16 * (lane & 3));
           const uint32_t v4[4] = {vp.x, vp.y, vp.z, vp.w};
@@ -743,19 +808,23 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const DecodeA
     }
   } else if (warp == kCopyWarp) {
     // ------------------------------------------------------------------ copies
-    auto page_of = [&](int ti) {  // page of a 16-position tile; the next unit's is read one unit ahead
-      int lp, tin;
-      tile_page(a, ti, &lp, &tin);
-      return ti < s.grp.te ? a.page_table[static_cast<size_t>(s.grp.b0) * a.stride + lp] : 0;
-    };
-    while (walk.next(a, s)) {
-      int page = lane < 8 ? page_of(s16 + static_cast<int>(s.c - s.us) * 8 + lane) : 0;
-      for (u32 c = s.c; c < s.ce; ++c, ++i) {
+    while (walk_next<G>(a, sm.plan, s, lane)) {
+      const int te = s.te;
+      const int32_t* row = a.page_table + static_cast<size_t>(s.b0) * a.stride;
+      const uint8_t* head = a.pool + static_cast<size_t>(s.g) * (a.P / 16) * Gm::T4B;
+      auto page_of = [&](int ti) {  // page of a 16-position tile; the next unit's is read one unit ahead
+        int lp, tin;
+        tile_page(a, ti, &lp, &tin);
+        return lane < 8 && ti < te ? row[lp] : 0;
+      };
+      int ti = (s.p0 >> 4) + lane, page = page_of(ti);
+      const u32 i1 = i + uniform(s.n);
+#pragma unroll 1
+      for (; i != i1; ++i, ti += 8) {
         const int st = static_cast<int>(i % kRaw);
-        const int ti = s16 + static_cast<int>(c - s.us) * 8 + lane;
-        const int next = (lane < 8 && c + 1 < s.ce) ? page_of(ti + 8) : 0;
+        const int next = i + 1 != i1 ? page_of(ti + 8) : 0;
         if (i >= kRaw) wait(&sm.raw_empty[st], i / kRaw - 1);
-        const bool in = lane < 8 && ti < s.grp.te, good = in && page >= 0 && page < a.max_pages && !*abort;
+        const bool in = lane < 8 && ti < te, good = in && page >= 0 && page < a.max_pages && !*abort;
         if (in && !good && !*abort) atomicOr(a.err, KV4_DEVERR_PAGE_RANGE);
         const uint32_t ok = __ballot_sync(FULL, good);
         if (lane == 0) {
@@ -767,8 +836,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const DecodeA
           int lp, tin;
           tile_page(a, ti, &lp, &tin);
           bulk_g2s(sm.raw[st] + lane * Gm::T4B,
-                   a.pool + static_cast<size_t>(page) * a.page_bytes + (static_cast<size_t>(s.g) * (a.P / 16) + tin) * Gm::T4B, Gm::T4B,
-                   &sm.raw_full[st]);
+                   head + static_cast<size_t>(page) * a.page_bytes + static_cast<size_t>(tin) * Gm::T4B, Gm::T4B, &sm.raw_full[st]);
         }
         page = next;
       }
@@ -778,51 +846,54 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const DecodeA
     write_rows<G>(a, sm.plan, lane);
   } else {
     // ------------------------------------------------------------------ matrix products
-    if (lane == 0) {
-      // the descriptors' low bits are the address in units of 16 bytes: steps are added to them
-      const uint64_t q_desc = tc::smem_desc(smem_u32(sm.Q), kRB * 16, 128), p_desc = tc::smem_desc(smem_u32(sm.P), 128, kTile * 16);
-      u32 seg = 0, first = 0;
-      uint32_t nmma = 0;
-      auto pv = [&](u32 k, bool acc) {  // products of unit k
-        const int bf = static_cast<int>(k & 1);
-        wait(&sm.p_ready[bf], k >> 1);
-        wait(&sm.v_ready[bf], k >> 1);
-        tc::fence_after();
-        if (!*abort) {
-          const uint32_t id = tc::idesc_f16(kTile, nmma, true);
-          const uint64_t b = p_desc + bf * (kRB * kTile * 2 / 16);
-          const uint32_t av = tm + C::V + (kTile / 2) * bf;
-#pragma unroll
-          for (int x = 0; x < kTile / 16; ++x) tc::mma_ts(tm + C::O, av + 8 * x, b + x * (256 / 16), id, acc || x > 0);
-        }
-        tc::commit(&sm.pv_done[bf]);
-      };
-      while (walk.next(a, s)) {
-        first = i;
-        wait(&sm.q_ready, seg++);
-        nmma = static_cast<uint32_t>((s.rows + 15) & ~15);
-        const uint32_t id = tc::idesc_f16(kTile, nmma, false);
-        for (u32 c = s.c; c < s.ce; ++c, ++i) {
+    // the descriptors' low bits are the address in units of 16 bytes: steps are added to them
+    const uint64_t q_desc = tc::smem_desc(smem_u32(sm.Q), kRB * 16, 128), p_desc = tc::smem_desc(smem_u32(sm.P), 128, kTile * 16);
+    u32 seg = 0;
+    while (walk_next<G>(a, sm.plan, s, lane)) {
+      const u32 i0 = i, i1 = i + uniform(s.n);
+      const uint32_t nmma = static_cast<uint32_t>((uniform(s.rows) + 15) & ~15);
+      const uint32_t id_s = tc::idesc_f16(kTile, nmma, false), id_o = tc::idesc_f16(kTile, nmma, true);
+      wait(&sm.q_ready, seg++);
+      // scores of unit i, then the products of the unit before; all lanes wait, one issues
+#pragma unroll 1
+      for (; i != i1 + 1; ++i) {
+        if (i != i1) {
           const int bf = static_cast<int>(i & 1);
           wait(&sm.k_ready[bf], i >> 1);
           if (i >= 2) wait(&sm.s_free[bf], (i >> 1) - 1);
           tc::fence_after();
-          if (!*abort) {
-            const uint32_t ak = tm + C::K + (D / 2) * bf, ds = tm + C::S + kRB * bf;
+          const uint32_t ak = tm + C::K + (D / 2) * bf, ds = tm + C::S + kRB * bf;
+          if (lane == 0) {
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x) tc::mma_ts(ds, ak + 8 * x, q_desc + x * (2 * kRB * 16 / 16), id, x > 0);
+            for (int x = 0; x < D / 16; ++x) tc::mma_ts(ds, ak + 8 * x, q_desc + x * (2 * kRB * 16 / 16), id_s, x > 0);
+            tc::commit(&sm.qk_done[bf]);
           }
-          tc::commit(&sm.qk_done[bf]);
-          if (i > first) pv(i - 1, i - 1 > first);
+          __syncwarp();
         }
-        pv(i - 1, i - 1 > first);
+        if (i != i0) {
+          const u32 k = i - 1;
+          const int bf = static_cast<int>(k & 1);
+          wait(&sm.p_ready[bf], k >> 1);
+          wait(&sm.v_ready[bf], k >> 1);
+          tc::fence_after();
+          const uint64_t b = p_desc + bf * (kRB * kTile * 2 / 16);
+          const uint32_t av = tm + C::V + (kTile / 2) * bf;
+          if (lane == 0) {
+#pragma unroll
+            for (int x = 0; x < kTile / 16; ++x) tc::mma_ts(tm + C::O, av + 8 * x, b + x * (256 / 16), id_o, k != i0 || x > 0);
+            tc::commit(&sm.pv_done[bf]);
+          }
+          __syncwarp();
+        }
       }
-      // the last products are done before TMEM is freed, however the loop ended
+      i = i1;
+    }
+    // the last products are done before TMEM is freed, however the loop ended
+    if (lane == 0)
       for (u32 k = i > 2 ? i - 2 : 0; k < i; ++k) {
         mbar_wait_bounded(&sm.qk_done[k & 1], (k >> 1) & 1u, a.err, kWaitLimitNs);
         mbar_wait_bounded(&sm.pv_done[k & 1], (k >> 1) & 1u, a.err, kWaitLimitNs);
       }
-    }
     __syncwarp();
   }
   tc::fence_before();
