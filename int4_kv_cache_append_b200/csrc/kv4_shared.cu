@@ -12,7 +12,7 @@
 // Keeping A in TMEM leaves shared memory to the packed tiles, Q and P; with the positions as the
 // MMA's rows its cost follows the number of query rows, and s_t and z_t are one thread's constants.
 //
-// A thread block is 26 warps: four softmax warpgroups (16 of the 64 columns each, a thread per
+// A thread block is 18 warps: two softmax warpgroups (32 of the 64 columns each, a thread per
 // position), a warpgroup unpacking keys, one unpacking values, a warp of bulk copies and a warp
 // that issues the MMAs; K, V, S and P have two buffers, the packed tiles four.  The running maximum
 // of a row is raised only when a logit exceeds it by more than 8 (P then stays below 2^8, far inside
@@ -151,10 +151,15 @@ __device__ void write_rows(const DecodeArgs& a, const Plan& p, int lane) {
 
 // ------------------------------------------------------------------ prefix attention
 
-constexpr int kSoftGroups = 4;   // softmax warpgroups: group g takes the 8-column chunks g and g + 4
+constexpr int kSoftGroups = 2;   // softmax warpgroups: group g takes the 8-column chunks g, g + kSoftGroups, ...
+constexpr int kChunks = kRB / 8 / kSoftGroups;
 constexpr int kSoftWarps = 4 * kSoftGroups, kKeyWarp0 = kSoftWarps, kValWarp0 = kKeyWarp0 + 4, kCopyWarp = kValWarp0 + 4,
               kMmaWarp = kCopyWarp + 1, kSoftThreads = 32 * kSoftWarps;
 constexpr int kPrefixThreads = 32 * (kMmaWarp + 1);
+// Registers a thread, of the 96 at launch (5 warps on a scheduler): what the unpacking warpgroups
+// give up goes to the softmax ones.
+constexpr int kSoftRegs = 120, kKeyRegs = 64, kValRegs = 80;
+static_assert(32 * kSoftWarps * kSoftRegs + 128 * (kKeyRegs + kValRegs) + 64 * 96 <= kPrefixThreads * 96, "registers of the launch");
 constexpr float kUnset = -1e30f;   // running maximum of a row that has seen no position
 constexpr float kGrow = 8.f;       // a logit this far above the running maximum raises it
 constexpr float kQShift = 64.f;    // queries enter fp16 times this: typical ones are then near one
@@ -179,7 +184,7 @@ struct SmemPrefix {
   float4 cst[kRB / 2];        // rows 2j, 2j + 1: sum(q), sum(q), -m, -m
   alignas(8) float mul[kRB];             // rows whose query had to be scaled down to fit fp16: the factor back
   alignas(16) float alpha[kRB];
-  float red[kSoftGroups][4][16];
+  float red[kSoftGroups][4][8 * kChunks];
   float2 ksz[kRaw][kTile];    // key scale (times the codes' and queries' powers of two) and zero
   alignas(16) uint32_t large[kRaw][4];    // the unit has values beyond fp16 (one word per warp that looked)
   int lim[kRB];               // end of the row's INT4 positions in the prefix
@@ -207,18 +212,31 @@ struct Cols {
 template <typename T>
 __device__ __forceinline__ T uniform(T x) { return __shfl_sync(FULL, x, 0); }
 
+// Up to 64 polls of a phase.
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+      "KV4_POLL_%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra KV4_DONE_%=;\n"
+      " add.u32 n, n, 1;\n setp.lt.u32 q, n, 64;\n @q bra KV4_POLL_%=;\n"
+      "KV4_DONE_%=:\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // A bounded wait that gives up when any warp of the block has: every role then runs its loop to the
-// end without waiting, so that all of them reach the end of the kernel.
+// end without waiting, so that all of them reach the end of the kernel.  A warpgroup waits by one
+// warp, the others at a hardware barrier: polls by every warp were half of the issued instructions.
 __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err, uint64_t limit_ns) {
-  if (unlikely(!mbar_try_wait(bar, parity))) {
-    uint64_t t0 = 0;
+  const uint32_t at = smem_u32(bar);
+  if (unlikely(!poll(at, parity))) {
+    const uint64_t t0 = global_timer_ns();
 #pragma unroll 1
-    for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
-      if (it & 63u) continue;
-      const uint64_t t = global_timer_ns();
-      if (t0 == 0) t0 = t;
+    for (uint32_t it = 1; !poll(at, parity); ++it) {
       if (*abort) return;
-      if (t - t0 > limit_ns || it >= kWaitLimitPolls) {
+      if (global_timer_ns() - t0 > limit_ns || it >= kWaitLimitPolls / 64) {
         *abort = 1;
         atomicOr(err, KV4_DEVERR_WAIT_LIMIT);
         return;
@@ -259,7 +277,7 @@ __device__ __forceinline__ void walk_start(Segment& s, const Plan& p, int lane) 
 }
 
 template <int G>
-__device__ __noinline__ bool walk_next(const DecodeArgs& a, const Plan& p, Segment& s, int lane) {
+__device__ __forceinline__ bool walk_next(const DecodeArgs& a, const Plan& p, Segment& s, int lane) {
   u32 c = s.at, unit0 = s.unit0, seg0 = s.seg0;
   int gr = s.gr;
   __syncwarp();
@@ -490,7 +508,6 @@ __device__ __noinline__ void soft_unit_slow(SmemPrefix<D>& sm, const SoftUnit u,
     }
     tc::wait_st();
   }
-  if (i >= 2) wait_bar(&sm.pv_done[u.bf], ((i >> 1) - 1) & 1u, &sm.abort, err, limit_ns);  // the buffer's last product
 #pragma unroll 1
   for (int k = 0; k < u.nch; ++k) {
     const int c0 = 8 * (u.wg + kSoftGroups * k);
@@ -553,6 +570,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
 
   if (warp < kSoftWarps) {
     // ------------------------------------------------------------------ softmax
+    tc::set_regs_up<kSoftRegs>();
     const int wg = warp >> 2, w4 = warp & 3, pos = 32 * w4 + lane, id = 1 + wg;
     const uint32_t quad = static_cast<uint32_t>(32 * w4) << 16;
     if (a.stall_test) wait(&sm.stall, 0);
@@ -631,32 +649,33 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
       // a scaled query takes every unit of the segment off the straight path, a row block without rows none
       const int lim_min = uniform(sm.scaled ? -1 : sm.edge), sinks = a.s;
       const int nch = uniform((((s.rows + 15) >> 4) * 2 - wg + kSoftGroups - 1) / kSoftGroups);  // this group's chunks: 0, 1 or 2
-      uint64_t l2[8];  // this position's share of the rows' sums, two rows a register pair
+      uint64_t l2[4 * kChunks];  // this position's share of the rows' sums, two rows a register pair
 #pragma unroll
-      for (int j = 0; j < 8; ++j) l2[j] = 0ull;
+      for (int j = 0; j < 4 * kChunks; ++j) l2[j] = 0ull;
 
       const u32 i0 = i, i1 = i + uniform(s.n);
 #pragma unroll 1
       for (int p0 = uniform(s.p0); i != i1; ++i, p0 += kTile) {
         const int st = static_cast<int>(i % kRaw), bf = static_cast<int>(i & 1);
-        wait(&sm.qk_done[bf], i >> 1);
+        // the unit's scores; products are issued in order, so the P buffer's last ones are done too
+        if (w4 == 0) wait(&sm.qk_done[bf], i >> 1);
+        group_sync(id);
         tc::fence_after();
         const uint32_t s_addr = tm + quad + C::S + kRB * bf;
         // off the straight path: positions that some row does not attend, scaled queries, large values
         const uint4 lg = *reinterpret_cast<const uint4*>(sm.large[st]);
         bool slow = uniform(lg.x | lg.y | lg.z | lg.w | (sm.ok[st] ^ 0xFFu)) != 0u || p0 < sinks || p0 + kTile > lim_min;
-        uint32_t pk[8];
         if (!slow) {
           const float2 sz = sm.ksz[st][pos];
           const uint64_t ks2 = tc::pack2(sz.x, sz.x), kz2 = tc::pack2(sz.y, sz.y);
-          uint32_t r[16];
+          uint32_t r[8 * kChunks];
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+          for (int k = 0; k < kChunks; ++k)
             if (k < nch) tc::ld8(s_addr + 8 * (wg + kSoftGroups * k), r + 8 * k);
           tc::wait_ld(r);
           float top = kNegInf;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
+          for (int k = 0; k < kChunks; ++k) {
             if (k >= nch) break;
             const float4* cst = &sm.cst[4 * (wg + kSoftGroups * k)];
 #pragma unroll
@@ -675,31 +694,29 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
           if (!slow) {
             tc::fence_before();
             warp_arrive(&sm.s_free[bf], lane);
+            __half* const pb = &sm.P[bf][wg * (kTile * 8) + pos * 8];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < kChunks; ++k) {
               if (k >= nch) break;
+              uint32_t pk[4];
 #pragma unroll
               for (int j = 4 * k; j < 4 * k + 4; ++j) {
                 const float x0 = exp2_fast(__uint_as_float(r[2 * j])), x1 = exp2_fast(__uint_as_float(r[2 * j + 1]));
                 l2[j] = tc::add2(l2[j], tc::pack2(x0, x1));
-                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[j]) : "f"(x1), "f"(x0));
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[j - 4 * k]) : "f"(x1), "f"(x0));
               }
+              *reinterpret_cast<uint4*>(pb + k * (kSoftGroups * kTile * 8)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
-            if (i >= 2) wait(&sm.pv_done[bf], (i >> 1) - 1);  // the buffer's last product
-            __half* const pb = &sm.P[bf][wg * (kTile * 8) + pos * 8];
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              if (k < nch) *reinterpret_cast<uint4*>(pb + k * (kSoftGroups * kTile * 8)) = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
           }
         }
         if (unlikely(slow)) {
-          float l[16];
+          float l[8 * kChunks];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) tc::unpack2(l2[j], l[2 * j], l[2 * j + 1]);
+          for (int j = 0; j < 4 * kChunks; ++j) tc::unpack2(l2[j], l[2 * j], l[2 * j + 1]);
           const bool voted = uniform(lg.x | lg.y | lg.z | lg.w | (sm.ok[st] ^ 0xFFu)) == 0u && p0 >= sinks && p0 + kTile <= lim_min;
           soft_unit_slow<D>(sm, SoftUnit{s_addr, tm + quad + C::O, wg, w4, lane, nch, st, bf, p0, i == i0, voted || i == i0}, a.s, i, l, a.err, a.wait_ns);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) l2[j] = tc::pack2(l[2 * j], l[2 * j + 1]);
+          for (int j = 0; j < 4 * kChunks; ++j) l2[j] = tc::pack2(l[2 * j], l[2 * j + 1]);
           tc::fence_before();
           warp_arrive(&sm.s_free[bf], lane);
         }
@@ -709,7 +726,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
       }
 
       // the segment's partial: O^T lane 8 k + a of this warp is dim 32 w4 + 4 a + k
-      wait(&sm.pv_done[(i - 1) & 1], (i - 1) >> 1);
+      if (w4 == 0) wait(&sm.pv_done[(i - 1) & 1], (i - 1) >> 1);
+      group_sync(id);
       tc::fence_after();
       float* part = a.ppart + static_cast<size_t>(s.slot) * kRB * kPartRow<D>;
       const int dim = 32 * w4 + 4 * (lane & 7) + (lane >> 3);
@@ -723,21 +741,23 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
         for (int j = 0; j < 8; ++j)
           if (c0 + j < s.rows && dim < D) part[(c0 + j) * kPartRow<D> + dim] = __uint_as_float(o[j]);
       }
-      // sums over the 128 positions: lanes j and j + 16 of each warp end with this group's column j
-      float l[16];
+      // sums over the 128 positions: lane j of each warp ends with this group's column j
+      float l[8 * kChunks];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) tc::unpack2(l2[j], l[2 * j], l[2 * j + 1]);
+      for (int j = 0; j < 4 * kChunks; ++j) tc::unpack2(l2[j], l[2 * j], l[2 * j + 1]);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) l[j] += __shfl_xor_sync(FULL, l[j], 16);
+      for (int o = 16; o >= 8 * kChunks; o >>= 1)
 #pragma unroll
-      for (int o = 8; o; o >>= 1)
+        for (int j = 0; j < 8 * kChunks; ++j) l[j] += __shfl_xor_sync(FULL, l[j], o);
+#pragma unroll
+      for (int o = 4 * kChunks; o; o >>= 1)
 #pragma unroll
         for (int j = 0; j < o; ++j) {
           const bool up = (lane & o) != 0;
           const float got = __shfl_xor_sync(FULL, up ? l[j] : l[j + o], o);
           l[j] = (up ? l[j + o] : l[j]) + got;
         }
-      if (lane < 16) sm.red[wg][w4][lane] = l[0];
+      if (lane < 8 * kChunks) sm.red[wg][w4][lane] = l[0];
       group_sync(id);
       const int n = 8 * (wg + kSoftGroups * (lane >> 3)) + (lane & 7);
       if (w4 == 0 && lane < 8 * nch && n < s.rows) {
@@ -750,6 +770,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
     }
   } else if (warp < kValWarp0) {
     // ------------------------------------------------------------------ keys
+    tc::set_regs_down<kKeyRegs>();
     const int w = warp - kKeyWarp0;
     const int pos = 32 * w + lane;
     // codes are c 2^-24 (rows 8-15 of a tile: 16 c 2^-24), queries times kQShift
@@ -760,8 +781,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
 #pragma unroll 1
       for (int at = uniform(s.p0) + pos; i != i1; ++i, at += kTile) {
         const int st = static_cast<int>(i % kRaw), bf = static_cast<int>(i & 1);
-        wait(&sm.raw_full[st], i / kRaw);
-        if (i >= 2) wait(&sm.qk_done[bf], (i >> 1) - 1);
+        if (w == 0) {
+          wait(&sm.raw_full[st], i / kRaw);
+          if (i >= 2) wait(&sm.qk_done[bf], (i >> 1) - 1);
+        }
+        group_sync(6);
         tc::fence_after();
         const uint8_t* tile = sm.raw[st] + (pos >> 4) * Gm::T4B + 16 * D + 4 * (pos & 15);
         const uint32_t kp = *reinterpret_cast<const uint32_t*>(tile), vp = *reinterpret_cast<const uint32_t*>(tile + 64);
@@ -778,6 +802,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
     }
   } else if (warp < kCopyWarp) {
     // ------------------------------------------------------------------ values
+    tc::set_regs_down<kValRegs>();
     const int w = warp - kValWarp0;
     while (walk_next<G>(a, sm.plan, s, lane)) {
       const int hi = attended_end<G>(a, s, cap, lane);
@@ -785,8 +810,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
 #pragma unroll 1
       for (int p0 = uniform(s.p0); i != i1; ++i, p0 += kTile) {
         const int st = static_cast<int>(i % kRaw), bf = static_cast<int>(i & 1);
-        wait(&sm.raw_full[st], i / kRaw);
-        if (i >= 2) wait(&sm.pv_done[bf], (i >> 1) - 1);
+        if (w == 0) {
+          wait(&sm.raw_full[st], i / kRaw);
+          if (i >= 2) wait(&sm.pv_done[bf], (i >> 1) - 1);
+        }
+        group_sync(7);
         tc::fence_after();
         const uint32_t ok = uniform(sm.ok[st]);
         if (32 * w < D) {

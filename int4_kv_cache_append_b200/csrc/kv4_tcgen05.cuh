@@ -69,6 +69,12 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// Registers of this warpgroup's threads (every warp of it, once).
+template <int N>
+__device__ __forceinline__ void set_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void set_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // 16 TMEM lanes from the address' lane, 32 columns: register 2i of thread t is lane t / 4, column
 // 4i + t % 4; register 2i + 1 the same column of lane t / 4 + 8.
 __device__ __forceinline__ void st_16x128b_x8(uint32_t addr, const uint32_t* r) {
