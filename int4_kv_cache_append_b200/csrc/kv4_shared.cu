@@ -12,11 +12,11 @@
 // Keeping A in TMEM leaves shared memory to the packed tiles, Q and P; with the positions as the
 // MMA's rows its cost follows the number of query rows, and s_t and z_t are one thread's constants.
 //
-// A thread block is 18 warps: two softmax warpgroups (32 of the 64 columns each, a thread per
+// A thread block is 26 warps: four softmax warpgroups (16 of the 64 columns each, a thread per
 // position), a warpgroup unpacking keys, one unpacking values, a warp of bulk copies and a warp
 // that issues the MMAs; K, V, S and P have two buffers, the packed tiles four.  The running maximum
-// of a row is raised only when a logit exceeds it by more than 8 (P then stays below 2^8, far inside
-// fp16): the first unit of a segment sets it, later ones seldom need the rescaling of O.
+// of a row is raised only when a logit exceeds it by more than 11 (P then stays below 2^11, and 16
+// times that inside fp16): the first unit of a segment sets it, later ones seldom rescale O.
 #include "kv4_decode_kernel.cuh"
 #include "kv4_quant.cuh"
 #include "kv4_tcgen05.cuh"
@@ -151,17 +151,12 @@ __device__ void write_rows(const DecodeArgs& a, const Plan& p, int lane) {
 
 // ------------------------------------------------------------------ prefix attention
 
-constexpr int kSoftGroups = 2;   // softmax warpgroups: group g takes the 8-column chunks g, g + kSoftGroups, ...
-constexpr int kChunks = kRB / 8 / kSoftGroups;
+constexpr int kSoftGroups = 4;   // softmax warpgroups: group g takes the 8-column chunks g, g + kSoftGroups, ...
 constexpr int kSoftWarps = 4 * kSoftGroups, kKeyWarp0 = kSoftWarps, kValWarp0 = kKeyWarp0 + 4, kCopyWarp = kValWarp0 + 4,
               kMmaWarp = kCopyWarp + 1, kSoftThreads = 32 * kSoftWarps;
 constexpr int kPrefixThreads = 32 * (kMmaWarp + 1);
-// Registers a thread, of the 96 at launch (5 warps on a scheduler): what the unpacking warpgroups
-// give up goes to the softmax ones.
-constexpr int kSoftRegs = 120, kKeyRegs = 64, kValRegs = 80;
-static_assert(32 * kSoftWarps * kSoftRegs + 128 * (kKeyRegs + kValRegs) + 64 * 96 <= kPrefixThreads * 96, "registers of the launch");
 constexpr float kUnset = -1e30f;   // running maximum of a row that has seen no position
-constexpr float kGrow = 8.f;       // a logit this far above the running maximum raises it
+constexpr float kGrow = 11.f;      // a logit this far (log2) above the running maximum raises it
 constexpr float kQShift = 64.f;    // queries enter fp16 times this: typical ones are then near one
 
 // The units of this thread block, segment by segment: every warp walks them on its own.  The state
@@ -181,18 +176,19 @@ struct SmemPrefix {
   uint8_t raw[kRaw][8 * Geo<D>::T4B];
   __half P[2][kRB * kTile];   // [row / 8][position][row % 8]: MN-major core matrices
   __half Q[kRB * D];          // [k / 8][row][k % 8]: K-major core matrices
+  __half ones[2][kTile * 16]; // A operands of the rows' sums: all 1, and all 1/16 for units of large values
   float4 cst[kRB / 2];        // rows 2j, 2j + 1: sum(q), sum(q), -m, -m
   alignas(8) float mul[kRB];             // rows whose query had to be scaled down to fit fp16: the factor back
   alignas(16) float alpha[kRB];
-  float red[kSoftGroups][4][8 * kChunks];
+  float red[kSoftGroups][4][kRB / kSoftGroups];
   float2 ksz[kRaw][kTile];    // key scale (times the codes' and queries' powers of two) and zero
-  alignas(16) uint32_t large[kRaw][4];    // the unit has values beyond fp16 (one word per warp that looked)
+  alignas(16) uint32_t odd[kRaw][4];  // per key warp (two tiles): bit 0 values beyond fp16, bits 1, 2 a tile was not copied
   int lim[kRB];               // end of the row's INT4 positions in the prefix
   int edge;                   // smallest lim of the rows
   int scaled;                 // some row has mul != 1
   uint32_t ok[kRaw];          // tiles of the buffer that were copied
   uint64_t raw_full[kRaw], raw_empty[kRaw];
-  uint64_t k_ready[2], v_ready[2], qk_done[2], s_free[2], p_ready[2], pv_done[2];
+  uint64_t k_ready[2], v_ready[2], qk_done[2], p_ready[2], pv_done[2];
   uint64_t q_ready;
   uint64_t stall;             // never arrived on (kv4_debug_force_wait_timeout)
   uint32_t tmem;
@@ -201,11 +197,11 @@ struct SmemPrefix {
   Segment seg[kPrefixThreads / 32];
 };
 
-// TMEM columns: keys and values as A operands (two fp16 a column), scores, outputs.
+// TMEM columns: keys and values as A operands (two fp16 a column), scores, outputs, sums.
 template <int D>
 struct Cols {
-  static constexpr int K = 0, V = 2 * (D / 2), S = V + 2 * (kTile / 2), O = S + 2 * kRB, All = 512;
-  static_assert(O + kRB <= All, "TMEM columns");
+  static constexpr int K = 0, V = 2 * (D / 2), S = V + 2 * (kTile / 2), O = S + 2 * kRB, L = O + kRB, All = 512;
+  static_assert(L + kRB <= All, "TMEM columns");
 };
 
 // The same value in every lane, known as such to the compiler: branches on it need no reconvergence.
@@ -382,11 +378,11 @@ __device__ __forceinline__ void unpack_values(const uint8_t* raw, uint32_t tmem,
   const __half2 sixteenth = __float2half2_rn(0.0625f);
   // the unit's instructions are few: the warps of all roles run from one instruction cache
 #pragma unroll 1
-  for (int blk = 0; blk < 2; ++blk) {  // 32 columns: 4 tiles
-    uint32_t r[2][16];
+  for (int blk = 0; blk < 4; ++blk) {  // 16 columns: 2 tiles
+    uint32_t r[2][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int T = 4 * blk + (i >> 1), half = i & 1;
+    for (int i = 0; i < 4; ++i) {
+      const int T = 2 * blk + (i >> 1), half = i & 1;
       const uint32_t x = *reinterpret_cast<const uint32_t*>(vw + T * Gm::T4B + half * 32 * Gm::CH);
       uint2 sz = *reinterpret_cast<const uint2*>(pp + T * Gm::T4B + half * 32);
       if (unlikely(part)) {
@@ -414,31 +410,34 @@ __device__ __forceinline__ void unpack_values(const uint8_t* raw, uint32_t tmem,
         r[k >> 1][2 * i + (k & 1)] = *reinterpret_cast<const uint32_t*>(&v);
       }
     }
-    tc::st_16x128b_x8(tmem + (static_cast<uint32_t>(32 * w) << 16) + 32 * blk, r[0]);
-    tc::st_16x128b_x8(tmem + (static_cast<uint32_t>(32 * w + 16) << 16) + 32 * blk, r[1]);
+    tc::st_16x128b_x4(tmem + (static_cast<uint32_t>(32 * w) << 16) + 16 * blk, r[0]);
+    tc::st_16x128b_x4(tmem + (static_cast<uint32_t>(32 * w + 16) << 16) + 16 * blk, r[1]);
   }
 }
 
 // What a softmax warp needs to find its unit.
 struct SoftUnit {
-  uint32_t s_addr, o_addr;  // scores and outputs of this warp's TMEM lanes
+  uint32_t tm;              // TMEM address of this warp's lanes
   int wg, w4, lane, nch;    // softmax group, warp in it, lane, the group's 8-column chunks
-  int st, bf, p0;           // buffers, first position of the unit
+  int p0;                   // first position of the unit
+  u32 i;                    // number of the unit
   bool first, raise;        // first unit of the segment; the running maxima have to be raised
 };
 
 // A unit off the straight path, for one warp of a softmax group (all four take it together): positions
 // that some row does not attend, scaled queries, values taken times 1/16, and running maxima to be
-// raised (outputs in TMEM are rescaled, after the MMAs that are adding to them).  Reads the scores,
-// leaves the probabilities in the P buffer and the positions' sums in l.  Kept out of the loop: the
-// loops of all roles share the instruction cache, and this one needs no registers there.
+// raised (what was summed so far is rescaled in TMEM, after the MMAs that are adding to it).  Reads
+// the scores and writes the unit's probabilities, over what the straight path may have left there.
+// Kept out of the loop: the loops of all roles run side by side from one instruction cache.
 template <int D>
-__device__ __noinline__ void soft_unit_slow(SmemPrefix<D>& sm, const SoftUnit u, int sinks, u32 i, float* l, uint32_t* err, uint64_t limit_ns) {
+__device__ __noinline__ void soft_unit_slow(SmemPrefix<D>& sm, const SoftUnit u, int sinks, uint32_t* err, uint64_t limit_ns) {
+  using C = Cols<D>;
+  const int st = static_cast<int>(u.i % kRaw), bf = static_cast<int>(u.i & 1);
   const int pos = 32 * u.w4 + u.lane, at = u.p0 + pos, id = 1 + u.wg;
-  const float2 sz = sm.ksz[u.st][pos];
-  const uint32_t ok = sm.ok[u.st];
-  const bool dead = !((ok >> (pos >> 4)) & 1u) || at < sinks;
-  const bool large = (sm.large[u.st][0] | sm.large[u.st][1] | sm.large[u.st][2] | sm.large[u.st][3]) != 0u;
+  const float2 sz = sm.ksz[st][pos];
+  const uint32_t scores = u.tm + C::S + kRB * bf;
+  const bool dead = ((sm.odd[st][u.w4] >> (1 + (u.lane >> 4))) & 1u) || at < sinks;
+  const bool large = ((sm.odd[st][0] | sm.odd[st][1] | sm.odd[st][2] | sm.odd[st][3]) & 1u) != 0u;
   auto logit = [&](int n, uint32_t s) {
     const float x = sm.mul[n] * fmaf(sz.x, __uint_as_float(s), sz.y * reinterpret_cast<const float*>(&sm.cst[n >> 1])[n & 1]);
     return dead || at >= sm.lim[n] ? kNegInf : x;
@@ -451,7 +450,7 @@ __device__ __noinline__ void soft_unit_slow(SmemPrefix<D>& sm, const SoftUnit u,
     for (int k = 0; k < u.nch; ++k) {
       const int c0 = 8 * (u.wg + kSoftGroups * k);
       uint32_t r[8];
-      tc::ld8(u.s_addr + c0, r);
+      tc::ld8(scores + c0, r);
       tc::wait_ld(r);
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = fmaxf(top, logit(c0 + j, r[j]) + neg_max(c0 + j));
@@ -464,7 +463,7 @@ __device__ __noinline__ void soft_unit_slow(SmemPrefix<D>& sm, const SoftUnit u,
     for (int k = 0; k < u.nch; ++k) {
       const int c0 = 8 * (u.wg + kSoftGroups * k);
       uint32_t r[8];
-      tc::ld8(u.s_addr + c0, r);
+      tc::ld8(scores + c0, r);
       tc::wait_ld(r);
       float x[8];
 #pragma unroll
@@ -488,43 +487,37 @@ __device__ __noinline__ void soft_unit_slow(SmemPrefix<D>& sm, const SoftUnit u,
     }
     group_sync(id);
     if (!u.first) {
-      wait_bar(&sm.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1u, &sm.abort, err, limit_ns);
+      wait_bar(&sm.pv_done[(u.i - 1) & 1], ((u.i - 1) >> 1) & 1u, &sm.abort, err, limit_ns);
       tc::fence_after();
-    }
 #pragma unroll 1
-    for (int k = 0; k < u.nch; ++k) {
-      const int c0 = 8 * (u.wg + kSoftGroups * k);
-      uint32_t r[8];
-      if (!u.first) {
-        tc::ld8(u.o_addr + c0, r);
+      for (int k = 0; k < 2 * u.nch; ++k) {  // outputs, then sums
+        const int c0 = 8 * (u.wg + kSoftGroups * (k >> 1));
+        const uint32_t addr = u.tm + ((k & 1) ? C::L : C::O) + c0;
+        uint32_t r[8];
+        tc::ld8(addr, r);
         tc::wait_ld(r);
-      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        l[8 * k + j] *= sm.alpha[c0 + j];
-        if (!u.first) r[j] = __float_as_uint(__uint_as_float(r[j]) * sm.alpha[c0 + j]);
+        for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * sm.alpha[c0 + j]);
+        tc::st8(addr, r);
       }
-      if (!u.first) tc::st8(u.o_addr + c0, r);
+      tc::wait_st();
     }
-    tc::wait_st();
   }
 #pragma unroll 1
   for (int k = 0; k < u.nch; ++k) {
     const int c0 = 8 * (u.wg + kSoftGroups * k);
     uint32_t r[8], pk[4];
-    tc::ld8(u.s_addr + c0, r);
+    tc::ld8(scores + c0, r);
     tc::wait_ld(r);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float x0 = exp2_fast(logit(c0 + 2 * j, r[2 * j]) + neg_max(c0 + 2 * j));
       const float x1 = exp2_fast(logit(c0 + 2 * j + 1, r[2 * j + 1]) + neg_max(c0 + 2 * j + 1));
-      l[8 * k + 2 * j] += x0;
-      l[8 * k + 2 * j + 1] += x1;
       __half2 t = __floats2half2_rn(x0, x1);
       if (large) t = __hmul2(t, __float2half2_rn(16.f));  // the unit's values were taken times 1/16
       pk[j] = *reinterpret_cast<const uint32_t*>(&t);
     }
-    *reinterpret_cast<uint4*>(&sm.P[u.bf][c0 * kTile + pos * 8]) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    *reinterpret_cast<uint4*>(&sm.P[bf][c0 * kTile + pos * 8]) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
   }
 }
 
@@ -548,7 +541,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
       mbar_init(&sm.k_ready[i], 4);
       mbar_init(&sm.v_ready[i], 4);
       mbar_init(&sm.qk_done[i], 1);
-      mbar_init(&sm.s_free[i], kSoftWarps);
       mbar_init(&sm.p_ready[i], kSoftWarps);
       mbar_init(&sm.pv_done[i], 1);
     }
@@ -558,6 +550,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
     sm.abort = 0;
   }
   if (warp == kMmaWarp) tc::alloc(&sm.tmem, C::All);
+  for (int k = tid; k < kTile * 16; k += kPrefixThreads) {
+    sm.ones[0][k] = __float2half_rn(1.f);
+    sm.ones[1][k] = __float2half_rn(0.0625f);
+  }
+  fence_proxy_async_smem();
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -570,7 +567,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
 
   if (warp < kSoftWarps) {
     // ------------------------------------------------------------------ softmax
-    tc::set_regs_up<kSoftRegs>();
     const int wg = warp >> 2, w4 = warp & 3, pos = 32 * w4 + lane, id = 1 + wg;
     const uint32_t quad = static_cast<uint32_t>(32 * w4) << 16;
     if (a.stall_test) wait(&sm.stall, 0);
@@ -649,10 +645,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
       // a scaled query takes every unit of the segment off the straight path, a row block without rows none
       const int lim_min = uniform(sm.scaled ? -1 : sm.edge), sinks = a.s;
       const int nch = uniform((((s.rows + 15) >> 4) * 2 - wg + kSoftGroups - 1) / kSoftGroups);  // this group's chunks: 0, 1 or 2
-      uint64_t l2[4 * kChunks];  // this position's share of the rows' sums, two rows a register pair
-#pragma unroll
-      for (int j = 0; j < 4 * kChunks; ++j) l2[j] = 0ull;
-
       const u32 i0 = i, i1 = i + uniform(s.n);
 #pragma unroll 1
       for (int p0 = uniform(s.p0); i != i1; ++i, p0 += kTile) {
@@ -661,116 +653,73 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
         if (w4 == 0) wait(&sm.qk_done[bf], i >> 1);
         group_sync(id);
         tc::fence_after();
-        const uint32_t s_addr = tm + quad + C::S + kRB * bf;
         // off the straight path: positions that some row does not attend, scaled queries, large values
-        const uint4 lg = *reinterpret_cast<const uint4*>(sm.large[st]);
-        bool slow = uniform(lg.x | lg.y | lg.z | lg.w | (sm.ok[st] ^ 0xFFu)) != 0u || p0 < sinks || p0 + kTile > lim_min;
-        if (!slow) {
+        const uint4 fl = *reinterpret_cast<const uint4*>(sm.odd[st]);
+        const bool odd = uniform(fl.x | fl.y | fl.z | fl.w) != 0u || p0 < sinks || p0 + kTile > lim_min || i == i0;
+        bool slow = odd;
+        if (!odd) {
           const float2 sz = sm.ksz[st][pos];
           const uint64_t ks2 = tc::pack2(sz.x, sz.x), kz2 = tc::pack2(sz.y, sz.y);
-          uint32_t r[8 * kChunks];
-#pragma unroll
-          for (int k = 0; k < kChunks; ++k)
-            if (k < nch) tc::ld8(s_addr + 8 * (wg + kSoftGroups * k), r + 8 * k);
-          tc::wait_ld(r);
+          const uint32_t scores = tm + quad + C::S + kRB * bf + 8 * wg;
+          const float4* cst = &sm.cst[4 * wg];
+          __half* pb = &sm.P[bf][wg * (kTile * 8) + pos * 8];
           float top = kNegInf;
+#pragma unroll 2
+          for (int k = 0; k < nch; ++k) {
+            uint32_t r[8], pk[4];
+            tc::ld8(scores + 8 * kSoftGroups * k, r);
+            tc::wait_ld(r);
 #pragma unroll
-          for (int k = 0; k < kChunks; ++k) {
-            if (k >= nch) break;
-            const float4* cst = &sm.cst[4 * (wg + kSoftGroups * k)];
-#pragma unroll
-            for (int j = 4 * k; j < 4 * k + 4; ++j) {  // logits minus the running maximum
-              const float4 cc = cst[j - 4 * k];
+            for (int j = 0; j < 4; ++j) {
+              // logits minus the running maximum, two rows at once
+              const float4 cc = cst[4 * kSoftGroups * k + j];
               const uint64_t sv = tc::pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
               const uint64_t x = tc::fma2(ks2, sv, tc::fma2(kz2, tc::pack2(cc.x, cc.y), tc::pack2(cc.z, cc.w)));
               float e0, e1;
               tc::unpack2(x, e0, e1);
-              r[2 * j] = __float_as_uint(e0);
-              r[2 * j + 1] = __float_as_uint(e1);
               top = tc::max3(top, e0, e1);
+              const float x0 = exp2_fast(e0), x1 = exp2_fast(e1);
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[j]) : "f"(x1), "f"(x0));
             }
+            *reinterpret_cast<uint4*>(pb + k * (kSoftGroups * kTile * 8)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
-          slow = uniform(static_cast<int>(group_or(id, top > kGrow))) != 0;
-          if (!slow) {
-            tc::fence_before();
-            warp_arrive(&sm.s_free[bf], lane);
-            __half* const pb = &sm.P[bf][wg * (kTile * 8) + pos * 8];
-#pragma unroll
-            for (int k = 0; k < kChunks; ++k) {
-              if (k >= nch) break;
-              uint32_t pk[4];
-#pragma unroll
-              for (int j = 4 * k; j < 4 * k + 4; ++j) {
-                const float x0 = exp2_fast(__uint_as_float(r[2 * j])), x1 = exp2_fast(__uint_as_float(r[2 * j + 1]));
-                l2[j] = tc::add2(l2[j], tc::pack2(x0, x1));
-                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[j - 4 * k]) : "f"(x1), "f"(x0));
-              }
-              *reinterpret_cast<uint4*>(pb + k * (kSoftGroups * kTile * 8)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            }
-          }
+          slow = uniform(static_cast<int>(group_or(id, top > kGrow))) != 0;  // then the unit is done again
         }
-        if (unlikely(slow)) {
-          float l[8 * kChunks];
-#pragma unroll
-          for (int j = 0; j < 4 * kChunks; ++j) tc::unpack2(l2[j], l[2 * j], l[2 * j + 1]);
-          const bool voted = uniform(lg.x | lg.y | lg.z | lg.w | (sm.ok[st] ^ 0xFFu)) == 0u && p0 >= sinks && p0 + kTile <= lim_min;
-          soft_unit_slow<D>(sm, SoftUnit{s_addr, tm + quad + C::O, wg, w4, lane, nch, st, bf, p0, i == i0, voted || i == i0}, a.s, i, l, a.err, a.wait_ns);
-#pragma unroll
-          for (int j = 0; j < 4 * kChunks; ++j) l2[j] = tc::pack2(l[2 * j], l[2 * j + 1]);
-          tc::fence_before();
-          warp_arrive(&sm.s_free[bf], lane);
-        }
+        if (unlikely(slow))
+          soft_unit_slow<D>(sm, SoftUnit{tm + quad, wg, w4, lane, nch, p0, i, i == i0, !odd || i == i0}, sinks, a.err, a.wait_ns);
         fence_proxy_async_smem();
         tc::fence_before();
         warp_arrive(&sm.p_ready[bf], lane);
       }
 
-      // the segment's partial: O^T lane 8 k + a of this warp is dim 32 w4 + 4 a + k
+      // the segment's partial: O^T lane 8 k + a of this warp is dim 32 w4 + 4 a + k; every lane of L has the sums
       if (w4 == 0) wait(&sm.pv_done[(i - 1) & 1], (i - 1) >> 1);
       group_sync(id);
       tc::fence_after();
       float* part = a.ppart + static_cast<size_t>(s.slot) * kRB * kPartRow<D>;
-      const int dim = 32 * w4 + 4 * (lane & 7) + (lane >> 3);
+      const int dim = 32 * w4 + 4 * (lane & 7) + (lane >> 3), rows = s.rows;
 #pragma unroll 1
       for (int k = 0; k < nch; ++k) {
         const int c0 = 8 * (wg + kSoftGroups * k);
-        uint32_t o[8];
+        uint32_t o[8], l[8];
         tc::ld8(tm + quad + C::O + c0, o);
+        tc::ld8(tm + quad + C::L + c0, l);
         tc::wait_ld(o);
+        tc::wait_ld(l);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c0 + j < s.rows && dim < D) part[(c0 + j) * kPartRow<D> + dim] = __uint_as_float(o[j]);
-      }
-      // sums over the 128 positions: lane j of each warp ends with this group's column j
-      float l[8 * kChunks];
-#pragma unroll
-      for (int j = 0; j < 4 * kChunks; ++j) tc::unpack2(l2[j], l[2 * j], l[2 * j + 1]);
-#pragma unroll
-      for (int o = 16; o >= 8 * kChunks; o >>= 1)
-#pragma unroll
-        for (int j = 0; j < 8 * kChunks; ++j) l[j] += __shfl_xor_sync(FULL, l[j], o);
-#pragma unroll
-      for (int o = 4 * kChunks; o; o >>= 1)
-#pragma unroll
-        for (int j = 0; j < o; ++j) {
-          const bool up = (lane & o) != 0;
-          const float got = __shfl_xor_sync(FULL, up ? l[j] : l[j + o], o);
-          l[j] = (up ? l[j + o] : l[j]) + got;
+        for (int j = 0; j < 8; ++j) {
+          float* row = part + (c0 + j) * kPartRow<D>;
+          if (c0 + j < rows && dim < D) row[dim] = __uint_as_float(o[j]);
+          if (c0 + j < rows && w4 == 0 && lane == j)
+            *reinterpret_cast<float2*>(row + D) =
+                make_float2(-reinterpret_cast<const float*>(&sm.cst[(c0 + j) >> 1])[2 + (j & 1)], __uint_as_float(l[j]));
         }
-      if (lane < 8 * kChunks) sm.red[wg][w4][lane] = l[0];
-      group_sync(id);
-      const int n = 8 * (wg + kSoftGroups * (lane >> 3)) + (lane & 7);
-      if (w4 == 0 && lane < 8 * nch && n < s.rows) {
-        const float m = -(reinterpret_cast<const float*>(&sm.cst[n >> 1])[2 + (n & 1)]);
-        *reinterpret_cast<float2*>(part + n * kPartRow<D> + D) =
-            make_float2(m, (sm.red[wg][0][lane] + sm.red[wg][1][lane]) + (sm.red[wg][2][lane] + sm.red[wg][3][lane]));
       }
       tc::fence_before();
       soft_sync();
     }
   } else if (warp < kValWarp0) {
     // ------------------------------------------------------------------ keys
-    tc::set_regs_down<kKeyRegs>();
     const int w = warp - kKeyWarp0;
     const int pos = 32 * w + lane;
     // codes are c 2^-24 (rows 8-15 of a tile: 16 c 2^-24), queries times kQShift
@@ -793,7 +742,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
         sm.ksz[st][pos] = make_float2(half_lo(kp) * unit, half_hi(kp));
         const bool large = ((sm.ok[st] >> (pos >> 4)) & 1u) && at >= a.s && at < hi && value_large(vp);
         const uint32_t any = __ballot_sync(FULL, large);
-        if (lane == 0) sm.large[st][w] = any;
+        if (lane == 0) sm.odd[st][w] = (any != 0u) | (((sm.ok[st] >> (2 * w)) & 3u) ^ 3u) << 1;
         warp_arrive(&sm.raw_empty[st], lane);
         tc::wait_st();
         tc::fence_before();
@@ -802,7 +751,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
     }
   } else if (warp < kCopyWarp) {
     // ------------------------------------------------------------------ values
-    tc::set_regs_down<kValRegs>();
     const int w = warp - kValWarp0;
     while (walk_next<G>(a, sm.plan, s, lane)) {
       const int hi = attended_end<G>(a, s, cap, lane);
@@ -875,8 +823,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
   } else {
     // ------------------------------------------------------------------ matrix products
     // the descriptors' low bits are the address in units of 16 bytes: steps are added to them
-    const uint64_t q_desc = tc::smem_desc(smem_u32(sm.Q), kRB * 16, 128), p_desc = tc::smem_desc(smem_u32(sm.P), 128, kTile * 16);
+    const uint64_t q_desc = tc::smem_desc(smem_u32(sm.Q), kRB * 16, 128), p_desc = tc::smem_desc(smem_u32(sm.P), 128, kTile * 16),
+                   one_desc = tc::smem_desc(smem_u32(sm.ones), kTile * 16, 128);
     u32 seg = 0;
+    const bool leader = lane == 0;
     while (walk_next<G>(a, sm.plan, s, lane)) {
       const u32 i0 = i, i1 = i + uniform(s.n);
       const uint32_t nmma = static_cast<uint32_t>((uniform(s.rows) + 15) & ~15);
@@ -888,15 +838,11 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
         if (i != i1) {
           const int bf = static_cast<int>(i & 1);
           wait(&sm.k_ready[bf], i >> 1);
-          if (i >= 2) wait(&sm.s_free[bf], (i >> 1) - 1);
           tc::fence_after();
           const uint32_t ak = tm + C::K + (D / 2) * bf, ds = tm + C::S + kRB * bf;
-          if (lane == 0) {
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x) tc::mma_ts(ds, ak + 8 * x, q_desc + x * (2 * kRB * 16 / 16), id_s, x > 0);
-            tc::commit(&sm.qk_done[bf]);
-          }
-          __syncwarp();
+          for (int x = 0; x < D / 16; ++x) tc::mma_ts(ds, ak + 8 * x, q_desc + x * (2 * kRB * 16 / 16), id_s, x > 0, leader);
+          tc::commit(&sm.qk_done[bf], leader);
         }
         if (i != i0) {
           const u32 k = i - 1;
@@ -906,12 +852,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
           tc::fence_after();
           const uint64_t b = p_desc + bf * (kRB * kTile * 2 / 16);
           const uint32_t av = tm + C::V + (kTile / 2) * bf;
-          if (lane == 0) {
+          const uint4 fl = *reinterpret_cast<const uint4*>(sm.odd[k % kRaw]);
+          const uint64_t one = one_desc + (uniform((fl.x | fl.y | fl.z | fl.w) & 1u) ? kTile * 16 * 2 / 16 : 0);
 #pragma unroll
-            for (int x = 0; x < kTile / 16; ++x) tc::mma_ts(tm + C::O, av + 8 * x, b + x * (256 / 16), id_o, k != i0 || x > 0);
-            tc::commit(&sm.pv_done[bf]);
+          for (int x = 0; x < kTile / 16; ++x) {
+            tc::mma_ts(tm + C::O, av + 8 * x, b + x * (256 / 16), id_o, k != i0 || x > 0, leader);
+            tc::mma_ss(tm + C::L, one, b + x * (256 / 16), id_o, k != i0 || x > 0, leader);
           }
-          __syncwarp();
+          tc::commit(&sm.pv_done[bf], leader);
         }
       }
       i = i1;
