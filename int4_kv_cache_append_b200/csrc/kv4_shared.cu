@@ -151,7 +151,8 @@ __device__ void write_rows(const DecodeArgs& a, const Plan& p, int lane) {
 
 // ------------------------------------------------------------------ prefix attention
 
-constexpr int kSoftGroups = 4;   // softmax warpgroups: group g takes the 8-column chunks g, g + kSoftGroups, ...
+constexpr int kSoftGroups = 4;   // softmax warpgroups: group g takes the 8-column chunks g and g + 4
+constexpr int kChunks = kRB / 8 / kSoftGroups;
 constexpr int kSoftWarps = 4 * kSoftGroups, kKeyWarp0 = kSoftWarps, kValWarp0 = kKeyWarp0 + 4, kCopyWarp = kValWarp0 + 4,
               kMmaWarp = kCopyWarp + 1, kSoftThreads = 32 * kSoftWarps;
 constexpr int kPrefixThreads = 32 * (kMmaWarp + 1);
@@ -176,7 +177,6 @@ struct SmemPrefix {
   uint8_t raw[kRaw][8 * Geo<D>::T4B];
   __half P[2][kRB * kTile];   // [row / 8][position][row % 8]: MN-major core matrices
   __half Q[kRB * D];          // [k / 8][row][k % 8]: K-major core matrices
-  __half ones[2][kTile * 16]; // A operands of the rows' sums: all 1, and all 1/16 for units of large values
   float4 cst[kRB / 2];        // rows 2j, 2j + 1: sum(q), sum(q), -m, -m
   alignas(8) float mul[kRB];             // rows whose query had to be scaled down to fit fp16: the factor back
   alignas(16) float alpha[kRB];
@@ -197,11 +197,11 @@ struct SmemPrefix {
   Segment seg[kPrefixThreads / 32];
 };
 
-// TMEM columns: keys and values as A operands (two fp16 a column), scores, outputs, sums.
+// TMEM columns: keys and values as A operands (two fp16 a column), scores, outputs.
 template <int D>
 struct Cols {
-  static constexpr int K = 0, V = 2 * (D / 2), S = V + 2 * (kTile / 2), O = S + 2 * kRB, L = O + kRB, All = 512;
-  static_assert(L + kRB <= All, "TMEM columns");
+  static constexpr int K = 0, V = 2 * (D / 2), S = V + 2 * (kTile / 2), O = S + 2 * kRB, All = 512;
+  static_assert(O + kRB <= All, "TMEM columns");
 };
 
 // The same value in every lane, known as such to the compiler: branches on it need no reconvergence.
@@ -426,11 +426,12 @@ struct SoftUnit {
 
 // A unit off the straight path, for one warp of a softmax group (all four take it together): positions
 // that some row does not attend, scaled queries, values taken times 1/16, and running maxima to be
-// raised (what was summed so far is rescaled in TMEM, after the MMAs that are adding to it).  Reads
-// the scores and writes the unit's probabilities, over what the straight path may have left there.
+// raised (outputs are rescaled in TMEM, after the MMAs that are adding to them).  Reads the scores,
+// writes the unit's probabilities over what the straight path may have left there, and adds them to
+// the positions' sums l.
 // Kept out of the loop: the loops of all roles run side by side from one instruction cache.
 template <int D>
-__device__ __noinline__ void soft_unit_slow(SmemPrefix<D>& sm, const SoftUnit u, int sinks, uint32_t* err, uint64_t limit_ns) {
+__device__ __noinline__ void soft_unit_slow(SmemPrefix<D>& sm, const SoftUnit u, int sinks, float* l, uint32_t* err, uint64_t limit_ns) {
   using C = Cols<D>;
   const int st = static_cast<int>(u.i % kRaw), bf = static_cast<int>(u.i & 1);
   const int pos = 32 * u.w4 + u.lane, at = u.p0 + pos, id = 1 + u.wg;
@@ -490,15 +491,17 @@ __device__ __noinline__ void soft_unit_slow(SmemPrefix<D>& sm, const SoftUnit u,
       wait_bar(&sm.pv_done[(u.i - 1) & 1], ((u.i - 1) >> 1) & 1u, &sm.abort, err, limit_ns);
       tc::fence_after();
 #pragma unroll 1
-      for (int k = 0; k < 2 * u.nch; ++k) {  // outputs, then sums
-        const int c0 = 8 * (u.wg + kSoftGroups * (k >> 1));
-        const uint32_t addr = u.tm + ((k & 1) ? C::L : C::O) + c0;
+      for (int k = 0; k < u.nch; ++k) {
+        const int c0 = 8 * (u.wg + kSoftGroups * k);
         uint32_t r[8];
-        tc::ld8(addr, r);
+        tc::ld8(u.tm + C::O + c0, r);
         tc::wait_ld(r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * sm.alpha[c0 + j]);
-        tc::st8(addr, r);
+        for (int j = 0; j < 8; ++j) {
+          r[j] = __float_as_uint(__uint_as_float(r[j]) * sm.alpha[c0 + j]);
+          l[8 * k + j] *= sm.alpha[c0 + j];
+        }
+        tc::st8(u.tm + C::O + c0, r);
       }
       tc::wait_st();
     }
@@ -513,6 +516,8 @@ __device__ __noinline__ void soft_unit_slow(SmemPrefix<D>& sm, const SoftUnit u,
     for (int j = 0; j < 4; ++j) {
       const float x0 = exp2_fast(logit(c0 + 2 * j, r[2 * j]) + neg_max(c0 + 2 * j));
       const float x1 = exp2_fast(logit(c0 + 2 * j + 1, r[2 * j + 1]) + neg_max(c0 + 2 * j + 1));
+      l[8 * k + 2 * j] += x0;
+      l[8 * k + 2 * j + 1] += x1;
       __half2 t = __floats2half2_rn(x0, x1);
       if (large) t = __hmul2(t, __float2half2_rn(16.f));  // the unit's values were taken times 1/16
       pk[j] = *reinterpret_cast<const uint32_t*>(&t);
@@ -550,11 +555,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
     sm.abort = 0;
   }
   if (warp == kMmaWarp) tc::alloc(&sm.tmem, C::All);
-  for (int k = tid; k < kTile * 16; k += kPrefixThreads) {
-    sm.ones[0][k] = __float2half_rn(1.f);
-    sm.ones[1][k] = __float2half_rn(0.0625f);
-  }
-  fence_proxy_async_smem();
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -645,6 +645,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
       // a scaled query takes every unit of the segment off the straight path, a row block without rows none
       const int lim_min = uniform(sm.scaled ? -1 : sm.edge), sinks = a.s;
       const int nch = uniform((((s.rows + 15) >> 4) * 2 - wg + kSoftGroups - 1) / kSoftGroups);  // this group's chunks: 0, 1 or 2
+      uint64_t l2[4 * kChunks];  // this position's share of the rows' sums, two rows a register pair
+#pragma unroll
+      for (int j = 0; j < 4 * kChunks; ++j) l2[j] = 0ull;
       const u32 i0 = i, i1 = i + uniform(s.n);
 #pragma unroll 1
       for (int p0 = uniform(s.p0); i != i1; ++i, p0 += kTile) {
@@ -664,35 +667,55 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
           const float4* cst = &sm.cst[4 * wg];
           __half* pb = &sm.P[bf][wg * (kTile * 8) + pos * 8];
           float top = kNegInf;
-#pragma unroll 2
-          for (int k = 0; k < nch; ++k) {
-            uint32_t r[8], pk[4];
-            tc::ld8(scores + 8 * kSoftGroups * k, r);
-            tc::wait_ld(r);
+          uint64_t x2[4 * kChunks];
+          uint32_t r[8 * kChunks];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+          for (int k = 0; k < kChunks; ++k)
+            if (k < nch) tc::ld8(scores + 8 * kSoftGroups * k, r + 8 * k);
+          tc::wait_ld(r);
+#pragma unroll
+          for (int k = 0; k < kChunks; ++k) {
+            if (k >= nch) break;
+            uint32_t pk[4];
+#pragma unroll
+            for (int j = 4 * k; j < 4 * k + 4; ++j) {
               // logits minus the running maximum, two rows at once
-              const float4 cc = cst[4 * kSoftGroups * k + j];
+              const float4 cc = cst[4 * kSoftGroups * k + j - 4 * k];
               const uint64_t sv = tc::pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
               const uint64_t x = tc::fma2(ks2, sv, tc::fma2(kz2, tc::pack2(cc.x, cc.y), tc::pack2(cc.z, cc.w)));
               float e0, e1;
               tc::unpack2(x, e0, e1);
               top = tc::max3(top, e0, e1);
               const float x0 = exp2_fast(e0), x1 = exp2_fast(e1);
-              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[j]) : "f"(x1), "f"(x0));
+              x2[j] = tc::pack2(x0, x1);
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[j - 4 * k]) : "f"(x1), "f"(x0));
             }
             *reinterpret_cast<uint4*>(pb + k * (kSoftGroups * kTile * 8)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
           slow = uniform(static_cast<int>(group_or(id, top > kGrow))) != 0;  // then the unit is done again
+          if (!slow) {
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k) {
+              if (k >= nch) break;
+#pragma unroll
+              for (int j = 4 * k; j < 4 * k + 4; ++j) l2[j] = tc::add2(l2[j], x2[j]);
+            }
+          }
         }
-        if (unlikely(slow))
-          soft_unit_slow<D>(sm, SoftUnit{tm + quad, wg, w4, lane, nch, p0, i, i == i0, !odd || i == i0}, sinks, a.err, a.wait_ns);
+        if (unlikely(slow)) {
+          float l[8 * kChunks];
+#pragma unroll
+          for (int j = 0; j < 4 * kChunks; ++j) tc::unpack2(l2[j], l[2 * j], l[2 * j + 1]);
+          soft_unit_slow<D>(sm, SoftUnit{tm + quad, wg, w4, lane, nch, p0, i, i == i0, !odd || i == i0}, sinks, l, a.err, a.wait_ns);
+#pragma unroll
+          for (int j = 0; j < 4 * kChunks; ++j) l2[j] = tc::pack2(l[2 * j], l[2 * j + 1]);
+        }
         fence_proxy_async_smem();
         tc::fence_before();
         warp_arrive(&sm.p_ready[bf], lane);
       }
 
-      // the segment's partial: O^T lane 8 k + a of this warp is dim 32 w4 + 4 a + k; every lane of L has the sums
+      // the segment's partial: O^T lane 8 k + a of this warp is dim 32 w4 + 4 a + k
       if (w4 == 0) wait(&sm.pv_done[(i - 1) & 1], (i - 1) >> 1);
       group_sync(id);
       tc::fence_after();
@@ -701,19 +724,35 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
 #pragma unroll 1
       for (int k = 0; k < nch; ++k) {
         const int c0 = 8 * (wg + kSoftGroups * k);
-        uint32_t o[8], l[8];
+        uint32_t o[8];
         tc::ld8(tm + quad + C::O + c0, o);
-        tc::ld8(tm + quad + C::L + c0, l);
         tc::wait_ld(o);
-        tc::wait_ld(l);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float* row = part + (c0 + j) * kPartRow<D>;
-          if (c0 + j < rows && dim < D) row[dim] = __uint_as_float(o[j]);
-          if (c0 + j < rows && w4 == 0 && lane == j)
-            *reinterpret_cast<float2*>(row + D) =
-                make_float2(-reinterpret_cast<const float*>(&sm.cst[(c0 + j) >> 1])[2 + (j & 1)], __uint_as_float(l[j]));
+        for (int j = 0; j < 8; ++j)
+          if (c0 + j < rows && dim < D) part[(c0 + j) * kPartRow<D> + dim] = __uint_as_float(o[j]);
+      }
+      // sums over the 128 positions: lanes j and j + 16 of each warp end with this group's column j
+      float l[8 * kChunks];
+#pragma unroll
+      for (int j = 0; j < 4 * kChunks; ++j) tc::unpack2(l2[j], l[2 * j], l[2 * j + 1]);
+      static_assert(8 * kChunks == 16, "two halves of a warp");
+#pragma unroll
+      for (int j = 0; j < 16; ++j) l[j] += __shfl_xor_sync(FULL, l[j], 16);
+#pragma unroll
+      for (int o = 8; o; o >>= 1)
+#pragma unroll
+        for (int j = 0; j < o; ++j) {
+          const bool up = (lane & o) != 0;
+          const float got = __shfl_xor_sync(FULL, up ? l[j] : l[j + o], o);
+          l[j] = (up ? l[j + o] : l[j]) + got;
         }
+      if (lane < 16) sm.red[wg][w4][lane] = l[0];
+      group_sync(id);
+      const int n = 8 * (wg + kSoftGroups * (lane >> 3)) + (lane & 7);
+      if (w4 == 0 && lane < 8 * nch && n < rows) {
+        const float m = -(reinterpret_cast<const float*>(&sm.cst[n >> 1])[2 + (n & 1)]);
+        *reinterpret_cast<float2*>(part + n * kPartRow<D> + D) =
+            make_float2(m, (sm.red[wg][0][lane] + sm.red[wg][1][lane]) + (sm.red[wg][2][lane] + sm.red[wg][3][lane]));
       }
       tc::fence_before();
       soft_sync();
@@ -823,8 +862,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
   } else {
     // ------------------------------------------------------------------ matrix products
     // the descriptors' low bits are the address in units of 16 bytes: steps are added to them
-    const uint64_t q_desc = tc::smem_desc(smem_u32(sm.Q), kRB * 16, 128), p_desc = tc::smem_desc(smem_u32(sm.P), 128, kTile * 16),
-                   one_desc = tc::smem_desc(smem_u32(sm.ones), kTile * 16, 128);
+    const uint64_t q_desc = tc::smem_desc(smem_u32(sm.Q), kRB * 16, 128), p_desc = tc::smem_desc(smem_u32(sm.P), 128, kTile * 16);
     u32 seg = 0;
     const bool leader = lane == 0;
     while (walk_next<G>(a, sm.plan, s, lane)) {
@@ -852,13 +890,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
           tc::fence_after();
           const uint64_t b = p_desc + bf * (kRB * kTile * 2 / 16);
           const uint32_t av = tm + C::V + (kTile / 2) * bf;
-          const uint4 fl = *reinterpret_cast<const uint4*>(sm.odd[k % kRaw]);
-          const uint64_t one = one_desc + (uniform((fl.x | fl.y | fl.z | fl.w) & 1u) ? kTile * 16 * 2 / 16 : 0);
 #pragma unroll
-          for (int x = 0; x < kTile / 16; ++x) {
-            tc::mma_ts(tm + C::O, av + 8 * x, b + x * (256 / 16), id_o, k != i0 || x > 0, leader);
-            tc::mma_ss(tm + C::L, one, b + x * (256 / 16), id_o, k != i0 || x > 0, leader);
-          }
+          for (int x = 0; x < kTile / 16; ++x) tc::mma_ts(tm + C::O, av + 8 * x, b + x * (256 / 16), id_o, k != i0 || x > 0, leader);
           tc::commit(&sm.pv_done[bf], leader);
         }
       }

@@ -6,10 +6,7 @@ query head and output element.  Inside the prefix the query is rounded to fp16, 
 Cov_p(k_i, v) / sqrt(D) and the log-sum by sum_i e_i q_i mean_p(k_i) / sqrt(D), at most 2^-11 times
 the sums of magnitudes; with d a bound of a logit's error the second order is below 2 d^2 times the
 mean distance of v from the output.  A probability and a value are rounded to fp16 (each at most
-2^-11 of p |v|, or 2^-25 absolute for a probability below fp16's normal range).  The sum takes the
-rounded probabilities too: it moves by at most 2^-11 of itself, so the log-sum by 2^-11 (the outputs'
-bound stands: numerator and sum take the same weights p (1 + e), |e| <= 2^-11, which moves the
-output by at most 2^-11 sum p |v - o| <= 2^-11 (sum p |v| + |o|), and |o| <= sum p |v|).  The fp32 and
+2^-11 of p |v|, or 2^-25 absolute for a probability below fp16's normal range).  The fp32 and
 integer steps are held to 2e-4 of the outputs' scale and 1e-4 of the log-sum."""
 import ctypes
 
@@ -148,11 +145,11 @@ def reference(r):
                 p /= total
                 o, km, d = p @ v, p @ k, u * (np.abs(k) @ qr).max()
                 cov = (k - km).T @ ((v - o) * p[:, None])
-                e = u * (qr @ np.abs(cov) + 3 * (p @ np.abs(v))) + 2 * d * d * (p @ np.abs(v - o)) + 2.0 ** -25 * np.abs(v).sum(0) / total
+                e = u * (qr @ np.abs(cov) + 2 * (p @ np.abs(v))) + 2 * d * d * (p @ np.abs(v - o)) + 2.0 ** -25 * np.abs(v).sum(0) / total
                 if cfg.rotate_values:  # rotated back: signed sums of a block's errors over h
                     e = np.repeat(e.reshape(-1, h).mean(1), h)
                 bo[b, j] = e + 2e-4 * max(1.0, np.abs(ref[b, j]).max())
-                bl[b, j] = u * (qr @ np.abs(km)) + d * d + u + 1e-4
+                bl[b, j] = u * (qr @ np.abs(km)) + d * d + 1e-4
     return ref, lse, bo, bl
 
 
