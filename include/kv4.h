@@ -380,8 +380,8 @@ typedef struct {
 kv4_status kv4_rope_table(const kv4_rope_config* cfg, float* table, void* stream);
 
 /* A table with the norms: head vector x becomes x r w, r = 1 / sqrt(mean of x^2 + eps), before the
- * rotation; a NULL weight leaves that norm out.  The sum of squares is taken in fp64, r rounded to
- * fp32, everything after it in fp32, rounded once to the output's type. */
+ * rotation; a NULL weight leaves that norm out.  All of it is fp32, the sum of squares a binary tree
+ * over the elements in order and the root correctly rounded, rounded once to the output's type. */
 typedef struct {
   const float* table;      /* device fp32 [max_pos][rotary_dim / 2][2], 16-byte aligned    */
   int max_pos;

@@ -245,7 +245,7 @@ kv4::RopeArgs rope_args(const kv4_rope_params* r, uint32_t* err) {
   a.qw = r->q_weight;
   a.kw = r->k_weight;
   a.w_dtype = r->weight_dtype;
-  a.eps = static_cast<double>(r->eps);
+  a.eps = r->eps;
   a.err = err;
   return a;
 }

@@ -52,7 +52,7 @@ struct RopeArgs {
   const void* qw;         // norm weights [D], NULL: no norm
   const void* kw;
   int w_dtype;
-  double eps;
+  float eps;
   const void *q, *k, *v;  // [T][heads][D], token strides in elements
   int q_dtype, k_dtype, v_dtype;
   long long q_stride, k_stride, v_stride;

@@ -1,6 +1,7 @@
 // kv4_quant.cuh -- the per-vector encoders of the append kernels and where their codes go in a page
-// tile or a side-cache row.  A warp holds one head vector: lane l has elements 4l..4l+3 (D = 128
-// uses all 32 lanes, D = 64 the first 16).  Bit-exact rules: the butterfly runs strides 1, 2, ...,
+// tile or a side-cache row.  kv4_append: a warp holds one head vector, lane l elements 4l..4l+3 (D =
+// 128 uses all 32 lanes, D = 64 the first 16).  kv4_append_rope (the functions with an 8): D / 8 lanes
+// hold one, lane l of the group elements 8l..8l+7, and a warp 2 or 4 vectors.  Bit-exact rules: the butterfly runs strides 1, 2, ...,
 // h/2 in that order with plain fp32 add/sub (a + b, a - b); the quantiser uses IEEE fp32 sub/div,
 // rint (ties to even) and directed fp16 conversions; min and max are taken as values (+0 for zero).
 #pragma once
@@ -218,6 +219,141 @@ __device__ __forceinline__ uint8_t* kbf_unit(uint8_t* tile, int r, int lane) {
   using Gm = Geo<D>;
   const int e = 4 * lane, c = e / Gm::EPT, u = (e % Gm::EPT) >> 3;
   return tile + r * 2 * D + c * 2 * Gm::EPT + ((u ^ bf16_swz(D, c, r)) << 4) + (e & 7) * 2;
+}
+
+// ------------------------------------------------------------------ eight elements a lane
+
+// All D / 8 lanes of a vector's group hold the result of these.
+template <int D>
+__device__ __forceinline__ float group_min(float v) {
+#pragma unroll
+  for (int o = D / 16; o; o >>= 1) v = fminf(v, __shfl_xor_sync(kFullWarp, v, o));
+  return v;
+}
+template <int D>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int o = D / 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullWarp, v, o));
+  return v;
+}
+
+__device__ __forceinline__ void flip_signs8(float (&x)[8], int gl, const uint32_t (&signs)[4]) {
+  if ((signs[0] | signs[1] | signs[2] | signs[3]) == 0u) return;
+  const uint32_t sb = (signs[gl >> 2] >> (8 * (gl & 3))) & 255u;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(__float_as_uint(x[e]) ^ (((sb >> e) & 1u) << 31));
+}
+
+// Sylvester block Hadamard on blocks of h, strides ascending, over the group's D elements.
+__device__ __forceinline__ void hadamard8(float (&x)[8], int gl, int h) {
+#pragma unroll
+  for (int st = 1; st < 8; st <<= 1) {
+    if (st >= h) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if ((e & st) == 0) {
+        const float a = x[e], b = x[e + st];
+        x[e] = __fadd_rn(a, b);
+        x[e + st] = __fsub_rn(a, b);
+      }
+  }
+  for (int st = 8; st < h; st <<= 1) {
+    const int m = st >> 3;
+    // the upper half of a pair gets o - x, the lower x + o: one rounding of o +- x either way
+    const float sg = (gl & m) ? -1.f : 1.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = __fmaf_rn(x[e], sg, __shfl_xor_sync(kFullWarp, x[e], m));
+  }
+}
+
+// rint(a / s), the IEEE quotient rounded to an integer, in the low bits of the result (two's
+// complement): adding 1.5 2^23 rounds to an integer and leaves it there.  q = a inv is within 128 2^-22
+// of the quotient, so away from the middle between two integers it rounds to the same one; near the
+// middle the division itself decides.
+__device__ __forceinline__ uint32_t rint_div(float q, float a, float s) {
+  constexpr float kRound = 12582912.f;
+  float u = __fadd_rn(q, kRound);
+  if (fabsf(q - __fsub_rn(u, kRound)) > 0.4999f) u = __fadd_rn(rintf(__fdiv_rn(a, s)), kRound);
+  return __float_as_uint(u);
+}
+
+// INT4 codes of the lane's 8 elements, element e in bits 4e..4e+3; parameters and *bad as quant_int4.
+template <int D>
+__device__ __forceinline__ uint32_t quant_int4_8(const float (&x)[8], uint32_t* sz, bool* bad) {
+  float mn = x[0], mx = x[0];
+#pragma unroll
+  for (int e = 1; e < 8; ++e) {
+    mn = fminf(mn, x[e]);
+    mx = fmaxf(mx, x[e]);
+  }
+  mn = __fadd_rn(group_min<D>(mn), 0.0f);
+  mx = __fadd_rn(group_max<D>(mx), 0.0f);
+  const __half zh = __float2half_rd(mn);
+  const float zf = __half2float(zh);
+  const __half sh = __float2half_ru(__fdiv_rn(__fsub_rn(mx, zf), 15.0f));
+  const float sf = __half2float(sh);
+  *bad = !(isfinite(zf) && isfinite(sf));
+  *sz = static_cast<uint32_t>(__half_as_ushort(sh)) | (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
+  if (sf == 0.0f || *bad) return 0u;
+  const float inv = __frcp_rn(sf);
+  uint32_t packed = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    // zero <= x and the scale was rounded up: a code is at most 15; a NaN takes code 0
+    const float d = __fsub_rn(x[e], zf);
+    packed |= (rint_div(fmaxf(d * inv, 0.f), d, sf) & 15u) << (4 * e);
+  }
+  return packed;
+}
+
+// Symmetric INT8 codes, elements 0..3 in .x, 4..7 in .y.
+template <int D>
+__device__ __forceinline__ uint2 quant_int8_8(const float (&x)[8], uint16_t* sc, bool* bad) {
+  float a = fabsf(x[0]);
+#pragma unroll
+  for (int e = 1; e < 8; ++e) a = fmaxf(a, fabsf(x[e]));
+  a = group_max<D>(a);
+  const __half sh = __float2half_ru(__fdiv_rn(a, 127.0f));
+  const float sf = __half2float(sh);
+  *bad = !isfinite(sf);
+  *sc = __half_as_ushort(sh);
+  if (sf == 0.0f || *bad) return make_uint2(0u, 0u);
+  const float inv = __frcp_rn(sf);
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float q = x[e] * inv;  // at most 127 in magnitude; a NaN takes code 0
+    w[e >> 2] |= (rint_div(q == q ? q : 0.f, x[e], sf) & 0xffu) << (8 * (e & 3));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// The lane's 8 key elements of pair-row pr are one 8-byte group (even elements, then odd ones), both rows'.
+template <int D>
+__device__ __forceinline__ unsigned long long* k4_group(uint8_t* tile, int pr, int gl) {
+  const int unit = (gl >> 1) ^ (D >= 128 ? (pr & 1) : 0);
+  return reinterpret_cast<unsigned long long*>(tile + pr * D + 16 * unit + 8 * (gl & 1));
+}
+
+// Nibbles 0, 2, 4, 6 of x to the low nibbles of 4 bytes.
+__device__ __forceinline__ uint32_t spread_even(uint32_t x) {
+  return (x & 0xFu) | (x & 0xF00u) | (x & 0xF0000u) | (x & 0xF000000u);
+}
+
+template <int D>
+__device__ __forceinline__ void store_k4_8(uint8_t* tile, int r, int gl, uint32_t kc) {
+  unsigned long long* w = k4_group<D>(tile, r & 7, gl);
+  const unsigned long long codes = static_cast<unsigned long long>(spread_even(kc)) | (static_cast<unsigned long long>(spread_even(kc >> 4)) << 32);
+  const int sh = 4 * (r >> 3);
+  atomicAnd(w, ~(0x0F0F0F0F0F0F0F0Full << sh));
+  atomicOr(w, codes << sh);
+}
+
+template <int D>
+__device__ __forceinline__ void store_vbf_8(uint8_t* vblock, int r, int gl, const float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    *reinterpret_cast<__nv_bfloat16*>(vblock + vbf_offset<D>(r, 8 * gl + e)) = __float2bfloat16_rn(v[e]);
 }
 
 }  // namespace kv4

@@ -6,11 +6,10 @@
 //   (a, b) -> (a cos - b sin, b cos + a sin),
 // (a, b) = elements (i, i + R/2) (KV4_ROPE_HALF) or (2i, 2i + 1) (KV4_ROPE_INTERLEAVED) of the first
 // R elements; the others pass.  Before it, with a weight, x_j -> x_j r w_j, r = 1 / sqrt(mean x^2 + eps).
-// Every step is fixed so that the codes an append writes do not depend on the launch: the sum of
-// squares is taken in fp64 (exact for bf16 inputs of any one scale, so its order does not show),
-// r is its fp64 value rounded once to fp32, and the products and sums after it are single fp32
-// operations (no contraction).  The rotated key enters the cache's encoder in fp32: it is rounded
-// to no 16-bit type on the way.
+// Every step is a single fp32 operation in a fixed order (no contraction; the sum of squares is a
+// binary tree over the elements, the root IEEE-rounded), so that the codes an append writes do not
+// depend on the launch.  A sum in fp64 was 550 cycles of dependent latency a vector and the kernel's
+// bound.  The rotated key enters the cache's encoder in fp32: it is rounded to no 16-bit type on the way.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -27,33 +26,60 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int kThreads = 256;
 constexpr int kWarpsPerBlock = kThreads / 32;
 
-// Four consecutive elements of any of the three types.
-__device__ __forceinline__ void load4_any(const void* base, int dtype, long long i, float (&x)[4]) {
+// Eight consecutive elements of any of the three types (16-bit: one 16-byte access).
+__device__ __forceinline__ void load8(const void* base, int dtype, long long i, float (&x)[8]) {
   if (dtype == KV4_F32) {
-    load4<float>(base, static_cast<size_t>(i), x);
-  } else if (dtype == KV4_BF16) {
-    load4<__nv_bfloat16>(base, static_cast<size_t>(i), x);
-  } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(reinterpret_cast<const __half*>(base) + i);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
-    x[0] = a.x;
-    x[1] = a.y;
-    x[2] = b.x;
-    x[3] = b.y;
+    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + i);
+    const float4 u = p[0], v = p[1];
+    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+    x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+    return;
+  }
+  const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + i;
+  uint32_t w[4];
+  if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+  } else {  // rows of a fused projection may start on 8 bytes
+    const uint2 u = *reinterpret_cast<const uint2*>(p), v = *reinterpret_cast<const uint2*>(p + 4);
+    w[0] = u.x; w[1] = u.y; w[2] = v.x; w[3] = v.y;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (dtype == KV4_BF16) {
+      x[2 * j] = __uint_as_float(w[j] << 16);
+      x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+      x[2 * j] = f.x;
+      x[2 * j + 1] = f.y;
+    }
   }
 }
 
-__device__ __forceinline__ void store4_any(void* base, int dtype, long long i, const float (&x)[4]) {
+__device__ __forceinline__ void store8(void* base, int dtype, long long i, const float (&x)[8]) {
   if (dtype == KV4_F32) {
-    *reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + i) = make_float4(x[0], x[1], x[2], x[3]);
-  } else if (dtype == KV4_BF16) {
-    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(base) + i) =
-        make_uint2(pack_bf2(__float2bfloat16_rn(x[0]), __float2bfloat16_rn(x[1])),
-                   pack_bf2(__float2bfloat16_rn(x[2]), __float2bfloat16_rn(x[3])));
+    float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + i);
+    p[0] = make_float4(x[0], x[1], x[2], x[3]);
+    p[1] = make_float4(x[4], x[5], x[6], x[7]);
+    return;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (dtype == KV4_BF16) {
+      w[j] = pack_bf2(__float2bfloat16_rn(x[2 * j]), __float2bfloat16_rn(x[2 * j + 1]));
+    } else {
+      const __half2 h = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  uint16_t* p = reinterpret_cast<uint16_t*>(base) + i;
+  if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
-    const __half2 a = __floats2half2_rn(x[0], x[1]), b = __floats2half2_rn(x[2], x[3]);
-    *reinterpret_cast<uint2*>(reinterpret_cast<__half*>(base) + i) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(p + 4) = make_uint2(w[2], w[3]);
   }
 }
 
@@ -95,108 +121,124 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(RopeTableArgs a) {
 
 // ------------------------------------------------------------------ norm and rotation of one vector
 
-// A warp holds one head vector, lane l elements 4l..4l+3 (lanes < D/4).
+// D / 8 lanes hold one head vector, lane gl of the group elements 8 gl..8 gl + 7; a warp takes kPerWarp
+// vectors (heads of one token) at once.  Sixteen bytes a lane and half the shuffles of a vector
+// spread over the whole warp: the norm and rotation of 16383 tokens went from 206 us to 83.
+template <int D>
+constexpr int kLanes = D / 8;
+template <int D>
+constexpr int kPerWarp = 32 / kLanes<D>;
+
 template <int D>
 struct Rotation {
-  float c[4], s[4];  // of the lane's elements; s carries the sign of the partner's term
-  int src;           // lane of the half layout's partner
-  bool on;           // the lane's elements are among the first R
-  bool half;
+  float c[8], s[8];   // of the lane's elements; s carries the sign of the partner's term
+  int src_lo, src_hi; // lanes of the half layout's partners of elements 0..3 and 4..7
+  bool on;            // the lane's elements are among the first R
+  bool half, cross;   // half layout; its partner is four elements off (R / 2 not a multiple of 8)
 
   __device__ __forceinline__ void load(const RopeArgs& a, int pos, int lane) {
-    const int R = a.R;
+    const int R = a.R, gl = lane % kLanes<D>, base = lane - gl;
     half = a.layout == KV4_ROPE_HALF;
-    on = 4 * lane < R;
-    src = lane;
+    cross = ((R / 2) & 7) != 0;
+    on = 8 * gl < R;
+    src_lo = src_hi = lane;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       c[j] = 1.f;
       s[j] = 0.f;
     }
     if (!on) return;
     const float* row = a.table + static_cast<size_t>(pos) * R;
     if (half) {
-      const bool first = 8 * lane < R;
-      src = first ? lane + R / 8 : lane - R / 8;
-      const float4* t = reinterpret_cast<const float4*>(row + 2 * (first ? 4 * lane : 4 * lane - R / 2));
-      const float4 u = __ldg(t), v = __ldg(t + 1);
-      const float sg = first ? -1.f : 1.f;
-      c[0] = u.x; s[0] = sg * u.y; c[1] = u.z; s[1] = sg * u.w;
-      c[2] = v.x; s[2] = sg * v.y; c[3] = v.z; s[3] = sg * v.w;
+      const int m = R / 16;
+      const bool f0 = 16 * gl < R, f1 = 16 * gl + 8 < R;  // elements 0..3 and 4..7 are in the first half
+      src_lo = base + (f0 ? gl + m : gl - m - (cross ? 1 : 0));
+      src_hi = base + (f1 ? gl + m + (cross ? 1 : 0) : gl - m);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const bool first = q ? f1 : f0;
+        const int i = 8 * gl + 4 * q;
+        const float4* t = reinterpret_cast<const float4*>(row + 2 * (first ? i : i - R / 2));
+        const float4 u = __ldg(t), v = __ldg(t + 1);
+        const float sg = first ? -1.f : 1.f;
+        c[4 * q] = u.x; s[4 * q] = sg * u.y; c[4 * q + 1] = u.z; s[4 * q + 1] = sg * u.w;
+        c[4 * q + 2] = v.x; s[4 * q + 2] = sg * v.y; c[4 * q + 3] = v.z; s[4 * q + 3] = sg * v.w;
+      }
     } else {
-      const float4 u = __ldg(reinterpret_cast<const float4*>(row + 4 * lane));
-      c[0] = c[1] = u.x; s[0] = -u.y; s[1] = u.y;
-      c[2] = c[3] = u.z; s[2] = -u.w; s[3] = u.w;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float4 u = __ldg(reinterpret_cast<const float4*>(row + 8 * gl + 4 * q));
+        c[4 * q] = c[4 * q + 1] = u.x; s[4 * q] = -u.y; s[4 * q + 1] = u.y;
+        c[4 * q + 2] = c[4 * q + 3] = u.z; s[4 * q + 2] = -u.w; s[4 * q + 3] = u.w;
+      }
     }
   }
 
-  __device__ __forceinline__ void apply(float (&x)[4]) const {
-    float o[4];
-    if (half) {
+  __device__ __forceinline__ void apply(float (&x)[8]) const {
+    float o[8];
+    if (!half) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = __shfl_sync(FULL, x[j], src);
+      for (int j = 0; j < 8; ++j) o[j] = x[j ^ 1];
+    } else if (!cross) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = __shfl_sync(FULL, x[j], j < 4 ? src_lo : src_hi);
     } else {
-      o[0] = x[1];
-      o[1] = x[0];
-      o[2] = x[3];
-      o[3] = x[2];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = __shfl_sync(FULL, x[j ^ 4], j < 4 ? src_lo : src_hi);
     }
     if (on) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = __fadd_rn(__fmul_rn(x[j], c[j]), __fmul_rn(o[j], s[j]));
+      for (int j = 0; j < 8; ++j) x[j] = __fadd_rn(__fmul_rn(x[j], c[j]), __fmul_rn(o[j], s[j]));
     }
   }
 };
 
-// 1 / sqrt(ms) rounded to fp32: the hardware's fp32 estimate and one Newton step in fp64 (relative
-// error below 1e-13 before the rounding).  ms below or above the fp32 range goes by the fp64 root.
-__device__ __forceinline__ float rsqrt_rn(double ms) {
-  const float f = static_cast<float>(ms);
-  if (f > 1e-37f && f < 1e37f) {
-    const double y = static_cast<double>(rsqrtf(f));
-    return static_cast<float>(y * fma(-0.5 * ms * y, y, 1.5));
-  }
-  return static_cast<float>(1.0 / sqrt(ms));
-}
-
-// x r w over the warp's D elements.
+// x r w over the group's D elements.  The squares are summed as a binary tree over the elements in
+// order (neighbours first), in the lane and then across the group.
 template <int D>
-__device__ __forceinline__ void head_norm(float (&x)[4], const float (&w)[4], double eps) {
-  double ss = 0.0;
+__device__ __forceinline__ void head_norm(float (&x)[8], const float (&w)[8], float eps) {
+  float s[8];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) ss = fma(static_cast<double>(x[j]), static_cast<double>(x[j]), ss);
+  for (int j = 0; j < 8; ++j) s[j] = __fmul_rn(x[j], x[j]);
+  float ss = __fadd_rn(__fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3])), __fadd_rn(__fadd_rn(s[4], s[5]), __fadd_rn(s[6], s[7])));
 #pragma unroll
-  for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(FULL, ss, o);
-  const float r = rsqrt_rn(ss * (1.0 / D) + eps);
+  for (int o = 1; o < kLanes<D>; o <<= 1) ss = __fadd_rn(ss, __shfl_xor_sync(FULL, ss, o));
+  const float r = __frsqrt_rn(__fadd_rn(__fmul_rn(ss, 1.0f / D), eps));
 #pragma unroll
-  for (int j = 0; j < 4; ++j) x[j] = __fmul_rn(__fmul_rn(x[j], r), w[j]);
+  for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(__fmul_rn(x[j], r), w[j]);
 }
 
 template <int D>
-__device__ __forceinline__ void load_weight(const void* w, int dtype, int lane, float (&x)[4]) {
-  x[0] = x[1] = x[2] = x[3] = 1.f;
-  if (w && lane < D / 4) load4_any(w, dtype, 4 * lane, x);
+__device__ __forceinline__ void load_weight(const void* w, int dtype, int lane, float (&x)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = 1.f;
+  if (w) load8(w, dtype, 8 * (lane % kLanes<D>), x);
 }
 
-// n (<= kBatch) consecutive vectors, read before the first is worked on: norm, rotation, out.
-constexpr int kBatch = 4;
+// Heads h0.. (below h1) of one token, kBatch warp passes of kPerWarp heads at a time, whose loads are
+// issued before the first is worked on: norm, rotation, out.
+constexpr int kBatch = 2;
 template <int D>
-__device__ __forceinline__ void rope_vectors(const RopeArgs& a, const Rotation<D>& rot, const float (&w)[4], bool norm,
-                                             const void* in, int in_dt, long long i0, void* out, int out_dt, long long o0,
-                                             int n, int lane) {
-  const bool act = lane < D / 4;
-  float x[kBatch][4];
+__device__ __forceinline__ void rope_heads(const RopeArgs& a, const Rotation<D>& rot, const float (&w)[8], bool norm, const void* in,
+                                           int in_dt, long long i0, void* out, int out_dt, long long o0, int h0, int h1, int lane) {
+  const int mine = lane / kLanes<D>, e = 8 * (lane % kLanes<D>);
+  for (int h = h0; h < h1; h += kBatch * kPerWarp<D>) {
+    float x[kBatch][8];
 #pragma unroll
-  for (int u = 0; u < kBatch; ++u) {
-    x[u][0] = x[u][1] = x[u][2] = x[u][3] = 0.f;
-    if (act && u < n) load4_any(in, in_dt, i0 + u * D + 4 * lane, x[u]);
-  }
+    for (int u = 0; u < kBatch; ++u) {
+      const int k = h + u * kPerWarp<D> + mine;
 #pragma unroll
-  for (int u = 0; u < kBatch; ++u) {
-    if (u >= n) break;
-    if (norm) head_norm<D>(x[u], w, a.eps);
-    rot.apply(x[u]);
-    if (act) store4_any(out, out_dt, o0 + u * D + 4 * lane, x[u]);
+      for (int j = 0; j < 8; ++j) x[u][j] = 0.f;
+      if (k < h1) load8(in, in_dt, i0 + k * D + e, x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int k = h + u * kPerWarp<D> + mine;
+      if (h + u * kPerWarp<D> >= h1) break;
+      if (norm) head_norm<D>(x[u], w, a.eps);
+      rot.apply(x[u]);
+      if (k < h1) store8(out, out_dt, o0 + k * D + e, x[u]);
+    }
   }
 }
 
@@ -204,7 +246,7 @@ __device__ __forceinline__ void rope_vectors(const RopeArgs& a, const Rotation<D
 
 // Warp (token, run of hpw heads): queries first, then keys.
 template <int D>
-__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int hpw) {
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(RopeArgs a, int hpw) {
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int nq = (a.Hq + hpw - 1) / hpw, nk = (a.Hkv + hpw - 1) / hpw;
@@ -221,14 +263,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int hpw) {
   const void* weight = is_q ? a.qw : a.kw;
   Rotation<D> rot;
   rot.load(a, pos, lane);
-  float w[4];
+  float w[8];
   load_weight<D>(weight, a.w_dtype, lane, w);
-  const void* in = is_q ? a.q : a.k;
-  void* out = is_q ? a.q_out : a.k_out;
-  const int idt = is_q ? a.q_dtype : a.k_dtype, odt = is_q ? a.q_out_dtype : a.k_out_dtype;
-  const long long i0 = t * (is_q ? a.q_stride : a.k_stride), o0 = t * (is_q ? a.q_out_stride : a.k_out_stride);
-  for (int h = h0; h < h1; h += kBatch)
-    rope_vectors<D>(a, rot, w, weight != nullptr, in, idt, i0 + h * D, out, odt, o0 + h * D, min(kBatch, h1 - h), lane);
+  rope_heads<D>(a, rot, w, weight != nullptr, is_q ? a.q : a.k, is_q ? a.q_dtype : a.k_dtype, t * (is_q ? a.q_stride : a.k_stride),
+                is_q ? a.q_out : a.k_out, is_q ? a.q_out_dtype : a.k_out_dtype, t * (is_q ? a.q_out_stride : a.k_out_stride), h0, h1, lane);
 }
 
 // ------------------------------------------------------------------ kv4_append_rope
@@ -273,82 +311,91 @@ __device__ __forceinline__ uint8_t* side_tile_of(const AppendArgs& a, int b, int
          static_cast<size_t>(row >> 4) * T8;
 }
 
-// The key of one (token, KV head), normed and rotated, into the page and the side row (-1: none).
+// The key of one (token, KV head), normed and rotated, into the page and the side row (-1: none), by its
+// lane group; act: the group has a head (the others take part in the shuffles).
 template <int D, int FMT>
-__device__ __forceinline__ void put_key(const AppendArgs& a, const Place& p, int g, int row, int lane, float (&k)[4]) {
-  const bool act = lane < D / 4;
+__device__ __forceinline__ void put_key(const AppendArgs& a, const Place& p, int g, int row, int gl, bool act, float (&k)[8]) {
   uint8_t* tile = tile_of<D, FMT>(a, p, g);
   const int r = p.pos & 15;  // pages are multiples of 16 positions
   if constexpr (FMT == POOL_BF16) {
-    if (act)
-      *reinterpret_cast<uint2*>(kbf_unit<D>(tile, r, lane)) =
-          make_uint2(pack_bf2(__float2bfloat16_rn(k[0]), __float2bfloat16_rn(k[1])),
-                     pack_bf2(__float2bfloat16_rn(k[2]), __float2bfloat16_rn(k[3])));
-  } else {
-    flip_signs4(k, lane, a.signs);
-    hadamard4(k, lane, a.h);
-    uint32_t sz;
-    bool bad;
-    const uint32_t kc = quant_int4(k, act, &sz, &bad);
-    if (act) store_k4<D>(tile, r, lane, kc);
-    if (lane == 0) *reinterpret_cast<uint32_t*>(tile + (FMT == POOL_VBF ? 8 * D : 16 * D) + 4 * r) = sz;
-    bool bad8 = false;
-    if (row >= 0) {
-      uint8_t* t8 = side_tile_of<D, FMT>(a, p.b, g, row);
-      uint16_t sc;
-      const uint32_t k8 = quant_int8(k, act, &sc, &bad8);
-      if (act) *k8_word<D>(t8, row & 15, lane) = k8;
-      if (lane == 0) *reinterpret_cast<uint16_t*>(t8 + 16 * D + 2 * (row & 15)) = sc;
+    if (act) {
+      // both 4-element halves of the lane are in one 16-byte unit
+      uint4 w;
+      w.x = pack_bf2(__float2bfloat16_rn(k[0]), __float2bfloat16_rn(k[1]));
+      w.y = pack_bf2(__float2bfloat16_rn(k[2]), __float2bfloat16_rn(k[3]));
+      w.z = pack_bf2(__float2bfloat16_rn(k[4]), __float2bfloat16_rn(k[5]));
+      w.w = pack_bf2(__float2bfloat16_rn(k[6]), __float2bfloat16_rn(k[7]));
+      *reinterpret_cast<uint4*>(kbf_unit<D>(tile, r, 2 * gl)) = w;
     }
-    if (lane == 0 && (bad || bad8)) atomicOr(a.err, KV4_DEVERR_RANGE);
+  } else {
+    flip_signs8(k, gl, a.signs);
+    hadamard8(k, gl, a.h);
+    uint32_t sz;
+    bool bad, bad8 = false;
+    const uint32_t kc = quant_int4_8<D>(k, &sz, &bad);
+    if (act) {
+      store_k4_8<D>(tile, r, gl, kc);
+      if (gl == 0) *reinterpret_cast<uint32_t*>(tile + (FMT == POOL_VBF ? 8 * D : 16 * D) + 4 * r) = sz;
+    }
+    if (row >= 0) {
+      uint16_t sc;
+      const uint2 k8 = quant_int8_8<D>(k, &sc, &bad8);
+      if (act) {
+        uint8_t* t8 = side_tile_of<D, FMT>(a, p.b, g, row);
+        *reinterpret_cast<uint2*>(k8_word<D>(t8, row & 15, 2 * gl)) = k8;
+        if (gl == 0) *reinterpret_cast<uint16_t*>(t8 + 16 * D + 2 * (row & 15)) = sc;
+      }
+    }
+    if (act && gl == 0 && (bad || bad8)) atomicOr(a.err, KV4_DEVERR_RANGE);
   }
 }
 
 template <int D, int FMT>
-__device__ __forceinline__ void put_value(const AppendArgs& a, const Place& p, int g, int row, int lane, float (&v)[4]) {
-  const bool act = lane < D / 4;
+__device__ __forceinline__ void put_value(const AppendArgs& a, const Place& p, int g, int row, int gl, bool act, float (&v)[8]) {
   uint8_t* tile = tile_of<D, FMT>(a, p, g);
   const int r = p.pos & 15;
   if constexpr (FMT == POOL_BF16) {
-    if (act) store_vbf<D>(tile + 32 * D, r, lane, v);
+    if (act) store_vbf_8<D>(tile + 32 * D, r, gl, v);
   } else if constexpr (FMT == POOL_VBF) {
-    if (act) store_vbf<D>(tile + Geo<D>::VBO, r, lane, v);
-    if (act && row >= 0) store_vbf<D>(side_tile_of<D, FMT>(a, p.b, g, row) + Geo<D>::VB8O, row & 15, lane, v);
+    if (act) store_vbf_8<D>(tile + Geo<D>::VBO, r, gl, v);
+    if (act && row >= 0) store_vbf_8<D>(side_tile_of<D, FMT>(a, p.b, g, row) + Geo<D>::VB8O, row & 15, gl, v);
   } else {
     if (a.rotate_v) {
-      flip_signs4(v, lane, a.signs);
-      hadamard4(v, lane, a.h);
+      flip_signs8(v, gl, a.signs);
+      hadamard8(v, gl, a.h);
     }
     uint32_t sz;
     bool bad, bad8 = false;
-    const uint32_t vc = quant_int4(v, act, &sz, &bad);
-    if (act) *v4_chunk<D>(tile, r, lane) = static_cast<uint16_t>(vc);
-    if (lane == 0) *reinterpret_cast<uint32_t*>(tile + 16 * D + 64 + 4 * r) = sz;
-    if (row >= 0) {
-      uint8_t* vb = side_tile_of<D, FMT>(a, p.b, g, row) + Geo<D>::H8B;
-      uint16_t sc;
-      const uint32_t v8 = quant_int8(v, act, &sc, &bad8);
-      if (act) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) vb[v8_offset<D>(row & 15, 4 * lane + i)] = static_cast<uint8_t>(v8 >> (8 * i));
-      }
-      if (lane == 0) *reinterpret_cast<uint16_t*>(vb + 16 * D + 2 * (row & 15)) = sc;
+    const uint32_t vc = quant_int4_8<D>(v, &sz, &bad);
+    if (act) {
+      *v4_chunk<D>(tile, r, 2 * gl) = static_cast<uint16_t>(vc);
+      *v4_chunk<D>(tile, r, 2 * gl + 1) = static_cast<uint16_t>(vc >> 16);
+      if (gl == 0) *reinterpret_cast<uint32_t*>(tile + 16 * D + 64 + 4 * r) = sz;
     }
-    if (lane == 0 && (bad || bad8)) atomicOr(a.err, KV4_DEVERR_RANGE);
+    if (row >= 0) {
+      uint16_t sc;
+      const uint2 v8 = quant_int8_8<D>(v, &sc, &bad8);
+      if (act) {
+        uint8_t* vb = side_tile_of<D, FMT>(a, p.b, g, row) + Geo<D>::H8B;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) vb[v8_offset<D>(row & 15, 8 * gl + e)] = static_cast<uint8_t>((e < 4 ? v8.x : v8.y) >> (8 * (e & 3)));
+        if (gl == 0) *reinterpret_cast<uint16_t*>(vb + 16 * D + 2 * (row & 15)) = sc;
+      }
+    }
+    if (act && gl == 0 && (bad || bad8)) atomicOr(a.err, KV4_DEVERR_RANGE);
   }
 }
 
-// Warp (token, item): items are runs of hpw query heads, then the KV heads' keys, then their values
-// (mixed bit-width keys: key and value of a KV head together, they share a row record).
+// Warp (token, item): items are runs of hpw query heads, then passes of kPerWarp KV heads' keys, then
+// of their values (mixed bit-width keys: one KV head's key and value together, they share a record).
 template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads) append_rope_kernel(RopeArgs q, AppendArgs a, int hpw) {
-  constexpr int NI = D / 32;
+__global__ void __launch_bounds__(kThreads, 4) append_rope_kernel(RopeArgs q, AppendArgs a, int hpw) {
+  constexpr int NI = D / 32, HP = FMT == POOL_MIXED ? 1 : kPerWarp<D>;
   __shared__ uint32_t rows[FMT == POOL_MIXED ? kWarpsPerBlock : 1][2][kMixedRowWords<D>];
   __shared__ float xs[FMT == POOL_MIXED ? kWarpsPerBlock : 1][D];
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const bool act = lane < D / 4;
-  const int nq = (q.Hq + hpw - 1) / hpw, per = nq + (FMT == POOL_MIXED ? a.Hkv : 2 * a.Hkv);
+  const int lane = threadIdx.x & 31, gl = lane % kLanes<D>, mine = lane / kLanes<D>;
+  const int nq = (q.Hq + hpw - 1) / hpw, nkv = (a.Hkv + HP - 1) / HP, per = nq + (FMT == POOL_MIXED ? nkv : 2 * nkv);
   const int gw = static_cast<int>((blockIdx.x * static_cast<unsigned>(kThreads) + threadIdx.x) >> 5);
   const int t = gw / per, c = gw - t * per;
   if (t >= a.T) return;
@@ -358,32 +405,42 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(RopeArgs q, Appen
     if (lane == 0) atomicOr(a.err, KV4_DEVERR_LENGTH);
     return;
   }
-  Rotation<D> rot;
-  float w[4];
   if (c < nq) {
+    Rotation<D> rot;
+    float w[8];
     rot.load(q, p.pos, lane);
     load_weight<D>(q.qw, q.w_dtype, lane, w);
-    const int h1 = min((c + 1) * hpw, q.Hq);
-    for (int h = c * hpw; h < h1; h += kBatch)
-      rope_vectors<D>(q, rot, w, q.qw != nullptr, q.q, q.q_dtype, t * q.q_stride + h * D, q.q_out, q.q_out_dtype,
-                      t * q.q_out_stride + h * D, min(kBatch, h1 - h), lane);
+    rope_heads<D>(q, rot, w, q.qw != nullptr, q.q, q.q_dtype, t * q.q_stride, q.q_out, q.q_out_dtype, t * q.q_out_stride, c * hpw,
+                  min((c + 1) * hpw, q.Hq), lane);
     return;
   }
-  const bool is_k = FMT == POOL_MIXED || c < nq + a.Hkv;
-  const int g = is_k ? c - nq : c - nq - a.Hkv;
+  const bool is_k = FMT == POOL_MIXED || c < nq + nkv;
+  const int g0 = (is_k ? c - nq : c - nq - nkv) * HP, g = FMT == POOL_MIXED ? g0 : g0 + mine;
+  const bool act = FMT == POOL_MIXED ? mine == 0 : g < a.Hkv;
   const int row = FMT <= POOL_VBF ? side_row(p.pos, a.s, a.w, a.w > 0 && p.pos >= a.s ? a.lens_after[p.b] : 0) : -1;
-  float x[4] = {0.f, 0.f, 0.f, 0.f};
+  float x[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = 0.f;
   if (is_k) {
-    if (act) load4_any(q.k, q.k_dtype, t * q.k_stride + g * D + 4 * lane, x);
-    rot.load(q, p.pos, lane);
-    load_weight<D>(q.kw, q.w_dtype, lane, w);
-    if (q.kw) head_norm<D>(x, w, q.eps);
-    rot.apply(x);
+    if (act) load8(q.k, q.k_dtype, t * q.k_stride + g * D + 8 * gl, x);
+    if (q.kw) {
+      float w[8];
+      load_weight<D>(q.kw, q.w_dtype, lane, w);
+      head_norm<D>(x, w, q.eps);
+    }
+    {
+      Rotation<D> rot;
+      rot.load(q, p.pos, lane);
+      rot.apply(x);
+    }
     if constexpr (FMT == POOL_MIXED) {
       // the encoder's lanes hold coordinates l + 32 i
       const int warp = threadIdx.x >> 5;
       float k[NI], v[NI];
-      if (act) *reinterpret_cast<float4*>(&xs[warp][4 * lane]) = make_float4(x[0], x[1], x[2], x[3]);
+      if (act) {
+        *reinterpret_cast<float4*>(&xs[warp][8 * gl]) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(&xs[warp][8 * gl + 4]) = make_float4(x[4], x[5], x[6], x[7]);
+      }
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
@@ -392,26 +449,25 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(RopeArgs q, Appen
       }
       mixed_encode_store<D>(a, g, p.page, p.pos, lane, k, v, rows[warp][0], rows[warp][1]);
     } else {
-      put_key<D, FMT>(a, p, g, row, lane, x);
+      put_key<D, FMT>(a, p, min(g, a.Hkv - 1), row, gl, act, x);
     }
   } else if constexpr (FMT != POOL_MIXED) {
-    if (act) load4_any(q.v, q.v_dtype, t * q.v_stride + g * D + 4 * lane, x);
-    put_value<D, FMT>(a, p, g, row, lane, x);
+    if (act) load8(q.v, q.v_dtype, t * q.v_stride + g * D + 8 * gl, x);
+    put_value<D, FMT>(a, p, min(g, a.Hkv - 1), row, gl, act, x);
   }
 }
 
 // ------------------------------------------------------------------ kv4_gather
 
 // Inverse of the stored rotation: diag(s) H x / h.
-template <int D>
-__device__ __forceinline__ void unrotate4(const AppendArgs& a, int lane, float (&x)[4]) {
+__device__ __forceinline__ void unrotate8(const AppendArgs& a, int gl, float (&x)[8]) {
   if (a.h > 1) {
-    hadamard4(x, lane, a.h);
+    hadamard8(x, gl, a.h);
     const float ih = 1.f / static_cast<float>(a.h);  // a power of two: exact
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] *= ih;
+    for (int j = 0; j < 8; ++j) x[j] *= ih;
   }
-  flip_signs4(x, lane, a.signs);
+  flip_signs8(x, gl, a.signs);
 }
 
 __device__ __forceinline__ float2 scale_zero(const uint8_t* p) {
@@ -430,130 +486,113 @@ __device__ __forceinline__ uint32_t get_bits(const uint32_t* row, int o, int w) 
 }
 
 template <int D>
-__device__ __forceinline__ void read_vbf(const uint8_t* vblock, int r, int lane, float (&x)[4]) {
+__device__ __forceinline__ void read_vbf(const uint8_t* vblock, int r, int gl, float (&x)[8]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    x[j] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(vblock + vbf_offset<D>(r, 4 * lane + j)));
+  for (int j = 0; j < 8; ++j)
+    x[j] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(vblock + vbf_offset<D>(r, 8 * gl + j)));
 }
 
-// Key (or value) of one (token, KV head) as fp32, in its original basis.
+// Slice of a mixed-key page tile that holds the position.
+template <int D>
+__device__ __forceinline__ const uint8_t* slice_of(const AppendArgs& a, const Place& p, int g, int KR, int VR) {
+  return a.pool + static_cast<size_t>(p.page) * a.page_bytes + static_cast<size_t>(g) * static_cast<size_t>(a.P) * (KR + VR + 8) +
+         static_cast<size_t>((p.pos % a.P) >> 4) * 16 * (KR + VR + 8);
+}
+
+// Key of one (token, KV head) as fp32 in its original basis, by its lane group.
 template <int D, int FMT>
-__device__ __forceinline__ void read_key(const AppendArgs& a, const Place& p, int g, int row, int lane, float (&x)[4]) {
-  const bool act = lane < D / 4;
+__device__ __forceinline__ void read_key(const AppendArgs& a, const Place& p, int g, int row, int gl, float (&x)[8]) {
+  const int r = p.pos & 15;
   if constexpr (FMT == POOL_MIXED) {
-    const int KR = a.kbits * D / 8, VR = a.vbits * D / 8, pp = p.pos % a.P, rr = pp & 15;
-    const uint8_t* slice = a.pool + static_cast<size_t>(p.page) * a.page_bytes +
-                           static_cast<size_t>(g) * static_cast<size_t>(a.P) * (KR + VR + 8) +
-                           static_cast<size_t>(pp >> 4) * 16 * (KR + VR + 8);
-    const float ks = scale_zero(slice + 16 * (KR + VR) + 8 * rr).x;
+    const int KR = a.kbits * D / 8, VR = a.vbits * D / 8;
+    const uint8_t* slice = slice_of<D>(a, p, g, KR, VR);
+    const float ks = scale_zero(slice + 16 * (KR + VR) + 8 * r).x;
     const float* sig = rec_sigma<D>(a.alloc, g);
-    const uint8_t* wid = rec_width<D>(a.alloc, g);
-    int w[4] = {0, 0, 0, 0}, sum = 0;
-    if (act) {
+    const uint2 wb = *reinterpret_cast<const uint2*>(rec_width<D>(a.alloc, g) + (8 * gl) % (D / 2));
+    int w[8], sum = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sum += w[j] = wid[(4 * lane + j) % (D / 2)];
-    }
+    for (int j = 0; j < 8; ++j) sum += w[j] = static_cast<int>(((j < 4 ? wb.x : wb.y) >> (8 * (j & 3))) & 255u);
     int o = sum;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(FULL, o, d);
-      if (lane >= d) o += y;
+    for (int d = 1; d < kLanes<D>; d <<= 1) {
+      const int y = __shfl_up_sync(FULL, o, d, kLanes<D>);
+      if (gl >= d) o += y;
     }
     o -= sum;
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(slice + static_cast<size_t>(rr) * KR);
-    if (act) {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(slice + static_cast<size_t>(r) * KR);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t c = get_bits(src, o, w[j]);
-        o += w[j];
-        const float mid = __fadd_rn(static_cast<float>(2u * c + 1u) * (1.f / static_cast<float>(1 << w[j])), -1.f);
-        x[j] = w[j] ? __fmul_rn(__fmul_rn(ks, sig[(4 * lane + j) % (D / 2)]), mid) : 0.f;
-      }
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t c = get_bits(src, o, w[j]);
+      o += w[j];
+      const float mid = __fadd_rn(static_cast<float>(2u * c + 1u) * (1.f / static_cast<float>(1 << w[j])), -1.f);
+      x[j] = w[j] ? __fmul_rn(__fmul_rn(ks, sig[(8 * gl + j) % (D / 2)]), mid) : 0.f;
     }
+  } else if (FMT != POOL_BF16 && row >= 0) {
+    uint8_t* t8 = side_tile_of<D, FMT>(a, p.b, g, row);
+    const float sc = __half2float(*reinterpret_cast<const __half*>(t8 + 16 * D + 2 * (row & 15)));
+    const uint2 c = *reinterpret_cast<const uint2*>(k8_word<D>(t8, row & 15, 2 * gl));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = sc * static_cast<float>(static_cast<int8_t>((j < 4 ? c.x : c.y) >> (8 * (j & 3))));
+    unrotate8(a, gl, x);
   } else {
-    if (row >= 0) {
-      const uint8_t* t8 = side_tile_of<D, FMT>(a, p.b, g, row);
-      const float sc = __half2float(*reinterpret_cast<const __half*>(t8 + 16 * D + 2 * (row & 15)));
-      if (act) {
-        const uint32_t c = *k8_word<D>(const_cast<uint8_t*>(t8), row & 15, lane);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = sc * static_cast<float>(static_cast<int8_t>(c >> (8 * j)));
-      }
+    uint8_t* tile = tile_of<D, FMT>(a, p, g);
+    if constexpr (FMT == POOL_BF16) {
+      load8(kbf_unit<D>(tile, r, 2 * gl), KV4_BF16, 0, x);
     } else {
-      uint8_t* tile = tile_of<D, FMT>(a, p, g);
-      const int r = p.pos & 15;
-      if constexpr (FMT == POOL_BF16) {
-        if (act) load4<__nv_bfloat16>(kbf_unit<D>(tile, r, lane), 0, x);
-      } else {
-        const float2 sz = scale_zero(tile + (FMT == POOL_VBF ? 8 * D : 16 * D) + 4 * r);
-        if (act) {
-          const uint32_t* wd = k4_words<D>(tile, r & 7, lane);
-          const int sh = 16 * (lane & 1) + 4 * (r >> 3);
-          const uint32_t e = wd[0] >> sh, o = wd[1] >> sh;
-          x[0] = fmaf(sz.x, static_cast<float>(e & 15u), sz.y);
-          x[1] = fmaf(sz.x, static_cast<float>(o & 15u), sz.y);
-          x[2] = fmaf(sz.x, static_cast<float>((e >> 8) & 15u), sz.y);
-          x[3] = fmaf(sz.x, static_cast<float>((o >> 8) & 15u), sz.y);
-        }
-      }
+      const float2 sz = scale_zero(tile + (FMT == POOL_VBF ? 8 * D : 16 * D) + 4 * r);
+      const unsigned long long w = *k4_group<D>(tile, r & 7, gl) >> (4 * (r >> 3));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        x[j] = fmaf(sz.x, static_cast<float>(static_cast<uint32_t>(w >> (32 * (j & 1) + 8 * (j >> 1))) & 15u), sz.y);
+      unrotate8(a, gl, x);
     }
-    if constexpr (FMT != POOL_BF16) unrotate4<D>(a, lane, x);
   }
 }
 
 template <int D, int FMT>
-__device__ __forceinline__ void read_value(const AppendArgs& a, const Place& p, int g, int row, int lane, float (&x)[4]) {
-  const bool act = lane < D / 4;
+__device__ __forceinline__ void read_value(const AppendArgs& a, const Place& p, int g, int row, int gl, float (&x)[8]) {
+  const int r = p.pos & 15;
   if constexpr (FMT == POOL_MIXED) {
-    const int KR = a.kbits * D / 8, VR = a.vbits * D / 8, pp = p.pos % a.P, rr = pp & 15;
-    const uint8_t* slice = a.pool + static_cast<size_t>(p.page) * a.page_bytes +
-                           static_cast<size_t>(g) * static_cast<size_t>(a.P) * (KR + VR + 8) +
-                           static_cast<size_t>(pp >> 4) * 16 * (KR + VR + 8);
-    const float2 zr = scale_zero(slice + 16 * (KR + VR) + 8 * rr + 4);  // zero, range
+    const int KR = a.kbits * D / 8, VR = a.vbits * D / 8;
+    const uint8_t* slice = slice_of<D>(a, p, g, KR, VR);
+    const float2 zr = scale_zero(slice + 16 * (KR + VR) + 8 * r + 4);  // zero, range
     const float step = __fdiv_rn(zr.y, static_cast<float>((1 << a.vbits) - 1));
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(slice + 16 * static_cast<size_t>(KR) + static_cast<size_t>(rr) * VR);
-    if (act) {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(slice + 16 * static_cast<size_t>(KR) + static_cast<size_t>(r) * VR);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x[j] = fmaf(step, static_cast<float>(get_bits(src, (4 * lane + j) * a.vbits, a.vbits)), zr.x);
-    }
+    for (int j = 0; j < 8; ++j) x[j] = fmaf(step, static_cast<float>(get_bits(src, (8 * gl + j) * a.vbits, a.vbits)), zr.x);
   } else if (FMT != POOL_BF16 && row >= 0) {
-    const uint8_t* t8 = side_tile_of<D, FMT>(a, p.b, g, row);
+    uint8_t* t8 = side_tile_of<D, FMT>(a, p.b, g, row);
     if constexpr (FMT == POOL_VBF) {
-      if (act) read_vbf<D>(t8 + Geo<D>::VB8O, row & 15, lane, x);
+      read_vbf<D>(t8 + Geo<D>::VB8O, row & 15, gl, x);
     } else {
       const uint8_t* vb = t8 + Geo<D>::H8B;
       const float sc = __half2float(*reinterpret_cast<const __half*>(vb + 16 * D + 2 * (row & 15)));
-      if (act) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = sc * static_cast<float>(static_cast<int8_t>(vb[v8_offset<D>(row & 15, 4 * lane + j)]));
-      }
+      for (int j = 0; j < 8; ++j) x[j] = sc * static_cast<float>(static_cast<int8_t>(vb[v8_offset<D>(row & 15, 8 * gl + j)]));
     }
   } else {
     uint8_t* tile = tile_of<D, FMT>(a, p, g);
-    const int r = p.pos & 15;
     if constexpr (FMT == POOL_BF16) {
-      if (act) read_vbf<D>(tile + 32 * D, r, lane, x);
+      read_vbf<D>(tile + 32 * D, r, gl, x);
     } else if constexpr (FMT == POOL_VBF) {
-      if (act) read_vbf<D>(tile + Geo<D>::VBO, r, lane, x);
+      read_vbf<D>(tile + Geo<D>::VBO, r, gl, x);
     } else {
       const float2 sz = scale_zero(tile + 16 * D + 64 + 4 * r);
-      if (act) {
-        const uint32_t c = *v4_chunk<D>(tile, r, lane);
+      const uint32_t c = *v4_chunk<D>(tile, r, 2 * gl) | (static_cast<uint32_t>(*v4_chunk<D>(tile, r, 2 * gl + 1)) << 16);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = fmaf(sz.x, static_cast<float>((c >> (4 * j)) & 15u), sz.y);
-      }
+      for (int j = 0; j < 8; ++j) x[j] = fmaf(sz.x, static_cast<float>((c >> (4 * j)) & 15u), sz.y);
     }
   }
-  if (FMT == POOL_INT4 && a.rotate_v) unrotate4<D>(a, lane, x);
+  if (FMT == POOL_INT4 && a.rotate_v) unrotate8(a, gl, x);
 }
 
-// Warp (token, KV head).
+// Warp (token, kPerWarp KV heads).
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads) gather_kernel(AppendArgs a, void* k_out, void* v_out, int dtype) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, gl = lane % kLanes<D>;
+  const int per = (a.Hkv + kPerWarp<D> - 1) / kPerWarp<D>;
   const int gw = static_cast<int>((blockIdx.x * static_cast<unsigned>(kThreads) + threadIdx.x) >> 5);
-  const int t = gw / a.Hkv, g = gw - t * a.Hkv;
+  const int t = gw / per, g = (gw - t * per) * kPerWarp<D> + lane / kLanes<D>;
   if (t >= a.T) return;
   Place p;
   if (!place_of(a, t, lane, p)) return;
@@ -566,21 +605,23 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(AppendArgs a, void* k_
     }
     if (FMT <= POOL_VBF) row = side_row(p.pos, a.s, a.w, L);
   }
-  const long long o = (static_cast<long long>(t) * a.Hkv + g) * D + 4 * lane;
-  float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-  if (k_out) read_key<D, FMT>(a, p, g, row, lane, x);
-  if (v_out) read_value<D, FMT>(a, p, g, row, lane, y);
-  if (lane < D / 4) {
-    if (k_out) store4_any(k_out, dtype, o, x);
-    if (v_out) store4_any(v_out, dtype, o, y);
+  const int gr = min(g, a.Hkv - 1);  // lanes without a head read the last one
+  const long long o = (static_cast<long long>(t) * a.Hkv + g) * D + 8 * gl;
+  float x[8], y[8];
+  if (k_out) read_key<D, FMT>(a, p, gr, row, gl, x);
+  if (v_out) read_value<D, FMT>(a, p, gr, row, gl, y);
+  if (g < a.Hkv) {
+    if (k_out) store8(k_out, dtype, o, x);
+    if (v_out) store8(v_out, dtype, o, y);
   }
 }
 
 unsigned blocks_for(long long warps) { return static_cast<unsigned>((warps + kWarpsPerBlock - 1) / kWarpsPerBlock); }
 
-// Query heads a warp takes: one while the launch has fewer warps than the GPU holds (the latency
-// counts), a batch of four loads in flight otherwise.
-int heads_per_warp(long long vectors) { return vectors > 148LL * 64 ? kBatch : 1; }
+// Query heads a warp takes: one pass while the launch has fewer warps than the GPU holds (the latency
+// counts), kBatch passes' loads in flight otherwise.
+template <int D>
+int heads_per_warp(long long vectors) { return vectors > 148LL * 64 * kPerWarp<D> ? 2 * kBatch * kPerWarp<D> : kPerWarp<D>; }
 
 }  // namespace
 
@@ -591,19 +632,24 @@ cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_rope(const RopeArgs& a, int D, cudaStream_t st) {
-  const int hpw = heads_per_warp(static_cast<long long>(a.T) * (a.Hq + a.Hkv));
+template <int D>
+static void launch_rope_d(const RopeArgs& a, cudaStream_t st) {
+  const int hpw = heads_per_warp<D>(static_cast<long long>(a.T) * (a.Hq + a.Hkv));
   const unsigned grid = blocks_for(static_cast<long long>(a.T) * ((a.Hq + hpw - 1) / hpw + (a.Hkv + hpw - 1) / hpw));
+  rope_kernel<D><<<grid, kThreads, 0, st>>>(a, hpw);
+}
+
+cudaError_t launch_rope(const RopeArgs& a, int D, cudaStream_t st) {
   note_launches(1);
-  if (D == 128) rope_kernel<128><<<grid, kThreads, 0, st>>>(a, hpw);
-  else rope_kernel<64><<<grid, kThreads, 0, st>>>(a, hpw);
+  if (D == 128) launch_rope_d<128>(a, st);
+  else launch_rope_d<64>(a, st);
   return cudaGetLastError();
 }
 
 template <int D>
 static cudaError_t launch_append_rope_d(const RopeArgs& q, const AppendArgs& a, int format, cudaStream_t st) {
-  const int hpw = heads_per_warp(static_cast<long long>(a.T) * (q.Hq + 2 * a.Hkv));
-  const int per = (q.Hq + hpw - 1) / hpw + (format == POOL_MIXED ? a.Hkv : 2 * a.Hkv);
+  const int hpw = heads_per_warp<D>(static_cast<long long>(a.T) * (q.Hq + 2 * a.Hkv));
+  const int per = (q.Hq + hpw - 1) / hpw + (format == POOL_MIXED ? a.Hkv : 2 * ((a.Hkv + kPerWarp<D> - 1) / kPerWarp<D>));
   const unsigned grid = blocks_for(static_cast<long long>(a.T) * per);
   note_launches(1);
   switch (format) {
@@ -617,7 +663,7 @@ static cudaError_t launch_append_rope_d(const RopeArgs& q, const AppendArgs& a, 
 
 template <int D>
 static cudaError_t launch_gather_d(const AppendArgs& a, int format, void* k_out, void* v_out, int dtype, cudaStream_t st) {
-  const unsigned grid = blocks_for(static_cast<long long>(a.T) * a.Hkv);
+  const unsigned grid = blocks_for(static_cast<long long>(a.T) * ((a.Hkv + kPerWarp<D> - 1) / kPerWarp<D>));
   note_launches(1);
   switch (format) {
     case POOL_INT4: gather_kernel<D, POOL_INT4><<<grid, kThreads, 0, st>>>(a, k_out, v_out, dtype); break;

@@ -1,5 +1,6 @@
 """Rotary positions restated in NumPy: frequencies and tables in fp64, the norm and rotation step by
-step in fp32 (the sum of squares and the root in fp64, each product and sum rounded on its own)."""
+step in fp32 (the sum of squares a binary tree over neighbours, the root of its fp32 value correctly
+rounded, each product and sum rounded on its own)."""
 import math
 
 import numpy as np
@@ -43,8 +44,12 @@ def table64(freq, mult, max_pos):
 def norm32(x, w, eps):
     if w is None:
         return x
-    ms = (x.astype(np.float64) ** 2).sum(-1, keepdims=True) / x.shape[-1] + np.float64(np.float32(eps))
-    r = (1.0 / np.sqrt(ms)).astype(np.float32)
+    v = x * x
+    while v.shape[-1] > 1:
+        v = v[..., 0::2] + v[..., 1::2]
+    ms = v * np.float32(1.0 / x.shape[-1]) + np.float32(eps)
+    assert ms.dtype == np.float32
+    r = (1.0 / np.sqrt(ms.astype(np.float64))).astype(np.float32)
     return (x * r).astype(np.float32) * w.astype(np.float32)
 
 

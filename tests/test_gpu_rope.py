@@ -118,7 +118,7 @@ def test_rope_padding_and_bad_positions(kv4):
 
 
 def test_norm_extremes(kv4):
-    """Zero vectors, vectors whose squares leave the fp32 range, infinities."""
+    """Zero vectors, vectors whose squares leave the fp32 range (r is then 0, or 1 / sqrt(eps)), infinities."""
     D = 128
     w = torch.ones(D, device="cuda")
     x = rand((6, 1, D), "f32", 8)
