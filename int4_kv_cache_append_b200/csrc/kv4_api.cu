@@ -172,6 +172,7 @@ kv4::AppendArgs cache_args(const kv4_cache* c, int layer, int T, const int32_t* 
   a.T = T;
   a.Hkv = c->cfg.num_kv_heads;
   a.P = c->cfg.page_size;
+  a.p_shift = pow2(a.P) ? __builtin_ctz(static_cast<unsigned>(a.P)) : -1;
   a.s = int4 ? c->cfg.num_sinks : 0;
   a.w = int4 ? c->cfg.recent_window : 0;
   a.h = int4 ? c->cfg.hadamard_block : 1;

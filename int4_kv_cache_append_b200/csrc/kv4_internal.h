@@ -23,6 +23,7 @@ struct AppendArgs {
   const int32_t* page_table;
   int stride;
   int T, Hkv, P, s, w, h, max_seqs, max_pages, nt8;
+  int p_shift;            // log2(P) when P is a power of two, else -1
   size_t page_bytes, side_slot_bytes;
   uint32_t signs[4];      // bit d: key dim d negated before the rotation (randomised-sign Hadamard)
   int rotate_v;           // values stored in the keys' rotated basis too
@@ -60,6 +61,7 @@ struct RopeArgs {
   int q_out_dtype, k_out_dtype;
   long long q_out_stride, k_out_stride;
   const int32_t* pos;     // kv4_rope only
+  bool q_fast, k_fast;    // 16-bit rows on 16 bytes on both sides (set by the launchers)
   int T, Hq, Hkv;
   uint32_t* err;
 };

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(RopeTableArgs a) {
 
 // D / 8 lanes hold one head vector, lane gl of the group elements 8 gl..8 gl + 7; a warp takes kPerWarp
 // vectors (heads of one token) at once.  Sixteen bytes a lane and half the shuffles of a vector
-// spread over the whole warp: the norm and rotation of 16383 tokens went from 206 us to 83.
+// spread over the whole warp: the norm and rotation of 16383 tokens went from 206 us to 131.
 template <int D>
 constexpr int kLanes = D / 8;
 template <int D>
@@ -215,30 +215,82 @@ __device__ __forceinline__ void load_weight(const void* w, int dtype, int lane, 
   if (w) load8(w, dtype, 8 * (lane % kLanes<D>), x);
 }
 
-// Heads h0.. (below h1) of one token, kBatch warp passes of kPerWarp heads at a time, whose loads are
-// issued before the first is worked on: norm, rotation, out.
-constexpr int kBatch = 2;
+// Eight 16-bit elements to and from fp32.
+__device__ __forceinline__ void widen8(const uint4& u, bool bf16, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (bf16) {
+      x[2 * j] = __uint_as_float(w[j] << 16);
+      x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+      x[2 * j] = f.x;
+      x[2 * j + 1] = f.y;
+    }
+  }
+}
+__device__ __forceinline__ uint4 narrow8(const float (&x)[8], bool bf16) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (bf16) {
+      w[j] = pack_bf2(__float2bfloat16_rn(x[2 * j]), __float2bfloat16_rn(x[2 * j + 1]));
+    } else {
+      const __half2 h = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Both sides 16-bit with 16-byte rows (what a projection's output is).
+__host__ __device__ inline bool rows16(const void* in, int in_dt, long long in_stride, const void* out, int out_dt, long long out_stride) {
+  return in_dt != KV4_F32 && out_dt != KV4_F32 && ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15) == 0 &&
+         ((in_stride | out_stride) & 7) == 0;
+}
+
+// Heads h0.. (below h1) of one token: norm, rotation, out.  fast (rows16): the loads of kBatch warp
+// passes of kPerWarp heads are issued before the first is worked on (64 bytes a lane in flight; one
+// pass at a time, the kernel waited on memory: 131 us instead of 90 for 16383 tokens).
+constexpr int kBatch = 4;
 template <int D>
 __device__ __forceinline__ void rope_heads(const RopeArgs& a, const Rotation<D>& rot, const float (&w)[8], bool norm, const void* in,
-                                           int in_dt, long long i0, void* out, int out_dt, long long o0, int h0, int h1, int lane) {
+                                           int in_dt, long long i0, void* out, int out_dt, long long o0, int h0, int h1, bool fast, int lane) {
   const int mine = lane / kLanes<D>, e = 8 * (lane % kLanes<D>);
-  for (int h = h0; h < h1; h += kBatch * kPerWarp<D>) {
-    float x[kBatch][8];
+  if (fast) {
+    const uint16_t* src = reinterpret_cast<const uint16_t*>(in) + i0 + e;
+    uint16_t* dst = reinterpret_cast<uint16_t*>(out) + o0 + e;
+    const bool bi = in_dt == KV4_BF16, bo = out_dt == KV4_BF16;
+    for (int h = h0 + mine; h - mine < h1; h += kBatch * kPerWarp<D>) {
+      uint4 raw[kBatch];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int k = h + u * kPerWarp<D> + mine;
+      for (int u = 0; u < kBatch; ++u) {
+        const int k = h + u * kPerWarp<D>;
+        raw[u] = k < h1 ? __ldcs(reinterpret_cast<const uint4*>(src + k * D)) : make_uint4(0u, 0u, 0u, 0u);
+      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[u][j] = 0.f;
-      if (k < h1) load8(in, in_dt, i0 + k * D + e, x[u]);
+      for (int u = 0; u < kBatch; ++u) {
+        const int k = h + u * kPerWarp<D>;
+        if (k - mine >= h1) break;
+        float x[8];
+        widen8(raw[u], bi, x);
+        if (norm) head_norm<D>(x, w, a.eps);
+        rot.apply(x);
+        if (k < h1) *reinterpret_cast<uint4*>(dst + k * D) = narrow8(x, bo);
+      }
     }
+    return;
+  }
+#pragma unroll 1
+  for (int h = h0 + mine; h - mine < h1; h += kPerWarp<D>) {
+    float x[8];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int k = h + u * kPerWarp<D> + mine;
-      if (h + u * kPerWarp<D> >= h1) break;
-      if (norm) head_norm<D>(x[u], w, a.eps);
-      rot.apply(x[u]);
-      if (k < h1) store8(out, out_dt, o0 + k * D + e, x[u]);
-    }
+    for (int j = 0; j < 8; ++j) x[j] = 0.f;
+    if (h < h1) load8(in, in_dt, i0 + h * D + e, x);
+    if (norm) head_norm<D>(x, w, a.eps);
+    rot.apply(x);
+    if (h < h1) store8(out, out_dt, o0 + h * D + e, x);
   }
 }
 
@@ -246,7 +298,7 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a, const Rotation<D>&
 
 // Warp (token, run of hpw heads): queries first, then keys.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 4) rope_kernel(RopeArgs a, int hpw) {
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(RopeArgs a, int hpw) {
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int nq = (a.Hq + hpw - 1) / hpw, nk = (a.Hkv + hpw - 1) / hpw;
@@ -266,7 +318,8 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(RopeArgs a, int hpw) 
   float w[8];
   load_weight<D>(weight, a.w_dtype, lane, w);
   rope_heads<D>(a, rot, w, weight != nullptr, is_q ? a.q : a.k, is_q ? a.q_dtype : a.k_dtype, t * (is_q ? a.q_stride : a.k_stride),
-                is_q ? a.q_out : a.k_out, is_q ? a.q_out_dtype : a.k_out_dtype, t * (is_q ? a.q_out_stride : a.k_out_stride), h0, h1, lane);
+                is_q ? a.q_out : a.k_out, is_q ? a.q_out_dtype : a.k_out_dtype, t * (is_q ? a.q_out_stride : a.k_out_stride), h0, h1,
+                is_q ? a.q_fast : a.k_fast, lane);
 }
 
 // ------------------------------------------------------------------ kv4_append_rope
@@ -278,15 +331,19 @@ struct Place {
   int b, pos, page;
 };
 
+// Page-table column of a position, and the position in its page: by shift where P is a power of two.
+__device__ __forceinline__ int page_of(const AppendArgs& a, int pos) { return a.p_shift >= 0 ? pos >> a.p_shift : pos / a.P; }
+__device__ __forceinline__ int in_page(const AppendArgs& a, int pos) { return a.p_shift >= 0 ? pos & (a.P - 1) : pos % a.P; }
+
 __device__ __forceinline__ bool place_of(const AppendArgs& a, int t, int lane, Place& p) {
   p.b = a.seq_slot[t];
   p.pos = a.pos[t];
   if (p.b == -1) return false;  // a padding row
-  if (p.b < 0 || p.b >= a.max_seqs || p.pos < 0 || p.pos / a.P >= a.stride) {
+  if (p.b < 0 || p.b >= a.max_seqs || p.pos < 0 || page_of(a, p.pos) >= a.stride) {
     if (lane == 0) atomicOr(a.err, KV4_DEVERR_LENGTH);
     return false;
   }
-  p.page = a.page_table[static_cast<size_t>(p.b) * a.stride + p.pos / a.P];
+  p.page = a.page_table[static_cast<size_t>(p.b) * a.stride + page_of(a, p.pos)];
   if (p.page < 0 || p.page >= a.max_pages) {
     if (lane == 0) atomicOr(a.err, KV4_DEVERR_PAGE_RANGE);
     return false;
@@ -301,7 +358,7 @@ template <int D, int FMT>
 __device__ __forceinline__ uint8_t* tile_of(const AppendArgs& a, const Place& p, int g) {
   constexpr int PB = kPosBytes<D, FMT>;
   return a.pool + static_cast<size_t>(p.page) * a.page_bytes + static_cast<size_t>(g) * a.P * PB +
-         static_cast<size_t>((p.pos % a.P) >> 4) * (16 * PB);
+         static_cast<size_t>(in_page(a, p.pos) >> 4) * (16 * PB);
 }
 
 template <int D, int FMT>
@@ -386,16 +443,18 @@ __device__ __forceinline__ void put_value(const AppendArgs& a, const Place& p, i
   }
 }
 
-// Warp (token, item): items are runs of hpw query heads, then passes of kPerWarp KV heads' keys, then
-// of their values (mixed bit-width keys: one KV head's key and value together, they share a record).
+// Warp (token, item): items are runs of hpw query heads, then passes of kPerWarp KV heads: the key and
+// the value of each together with `joint` (one prologue and both loads in flight; many tokens), else
+// keys and values apart (few tokens: the latency counts).  Mixed bit-width keys: one KV head an item,
+// key and value share a record.
 template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads, 4) append_rope_kernel(RopeArgs q, AppendArgs a, int hpw) {
+__global__ void __launch_bounds__(kThreads, 3) append_rope_kernel(RopeArgs q, AppendArgs a, int hpw, bool joint) {
   constexpr int NI = D / 32, HP = FMT == POOL_MIXED ? 1 : kPerWarp<D>;
   __shared__ uint32_t rows[FMT == POOL_MIXED ? kWarpsPerBlock : 1][2][kMixedRowWords<D>];
   __shared__ float xs[FMT == POOL_MIXED ? kWarpsPerBlock : 1][D];
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, gl = lane % kLanes<D>, mine = lane / kLanes<D>;
-  const int nq = (q.Hq + hpw - 1) / hpw, nkv = (a.Hkv + HP - 1) / HP, per = nq + (FMT == POOL_MIXED ? nkv : 2 * nkv);
+  const int nq = (q.Hq + hpw - 1) / hpw, nkv = (a.Hkv + HP - 1) / HP, per = nq + (FMT == POOL_MIXED || joint ? nkv : 2 * nkv);
   const int gw = static_cast<int>((blockIdx.x * static_cast<unsigned>(kThreads) + threadIdx.x) >> 5);
   const int t = gw / per, c = gw - t * per;
   if (t >= a.T) return;
@@ -411,18 +470,17 @@ __global__ void __launch_bounds__(kThreads, 4) append_rope_kernel(RopeArgs q, Ap
     rot.load(q, p.pos, lane);
     load_weight<D>(q.qw, q.w_dtype, lane, w);
     rope_heads<D>(q, rot, w, q.qw != nullptr, q.q, q.q_dtype, t * q.q_stride, q.q_out, q.q_out_dtype, t * q.q_out_stride, c * hpw,
-                  min((c + 1) * hpw, q.Hq), lane);
+                  min((c + 1) * hpw, q.Hq), q.q_fast, lane);
     return;
   }
-  const bool is_k = FMT == POOL_MIXED || c < nq + nkv;
-  const int g0 = (is_k ? c - nq : c - nq - nkv) * HP, g = FMT == POOL_MIXED ? g0 : g0 + mine;
-  const bool act = FMT == POOL_MIXED ? mine == 0 : g < a.Hkv;
+  const bool is_k = FMT == POOL_MIXED || c < nq + nkv, is_v = FMT != POOL_MIXED && (joint || !is_k);
+  const int g0 = (is_k ? c - nq : c - nq - nkv) * HP, g = FMT == POOL_MIXED ? g0 : min(g0 + mine, a.Hkv - 1);
+  const bool act = FMT == POOL_MIXED ? mine == 0 : g0 + mine < a.Hkv;
   const int row = FMT <= POOL_VBF ? side_row(p.pos, a.s, a.w, a.w > 0 && p.pos >= a.s ? a.lens_after[p.b] : 0) : -1;
-  float x[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = 0.f;
+  float x[8], v[8];
+  if (is_v) load8(q.v, q.v_dtype, t * q.v_stride + g * D + 8 * gl, v);
   if (is_k) {
-    if (act) load8(q.k, q.k_dtype, t * q.k_stride + g * D + 8 * gl, x);
+    load8(q.k, q.k_dtype, t * q.k_stride + g * D + 8 * gl, x);
     if (q.kw) {
       float w[8];
       load_weight<D>(q.kw, q.w_dtype, lane, w);
@@ -436,24 +494,23 @@ __global__ void __launch_bounds__(kThreads, 4) append_rope_kernel(RopeArgs q, Ap
     if constexpr (FMT == POOL_MIXED) {
       // the encoder's lanes hold coordinates l + 32 i
       const int warp = threadIdx.x >> 5;
-      float k[NI], v[NI];
+      float k[NI], vv[NI];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) vv[i] = load_elem(q.v, q.v_dtype, static_cast<size_t>(t * q.v_stride + g * D + lane + 32 * i));
       if (act) {
         *reinterpret_cast<float4*>(&xs[warp][8 * gl]) = make_float4(x[0], x[1], x[2], x[3]);
         *reinterpret_cast<float4*>(&xs[warp][8 * gl + 4]) = make_float4(x[4], x[5], x[6], x[7]);
       }
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        k[i] = xs[warp][lane + 32 * i];
-        v[i] = load_elem(q.v, q.v_dtype, static_cast<size_t>(t * q.v_stride + g * D + lane + 32 * i));
-      }
-      mixed_encode_store<D>(a, g, p.page, p.pos, lane, k, v, rows[warp][0], rows[warp][1]);
+      for (int i = 0; i < NI; ++i) k[i] = xs[warp][lane + 32 * i];
+      mixed_encode_store<D>(a, g, p.page, p.pos, lane, k, vv, rows[warp][0], rows[warp][1]);
     } else {
-      put_key<D, FMT>(a, p, min(g, a.Hkv - 1), row, gl, act, x);
+      put_key<D, FMT>(a, p, g, row, gl, act, x);
     }
-  } else if constexpr (FMT != POOL_MIXED) {
-    if (act) load8(q.v, q.v_dtype, t * q.v_stride + g * D + 8 * gl, x);
-    put_value<D, FMT>(a, p, min(g, a.Hkv - 1), row, gl, act, x);
+  }
+  if constexpr (FMT != POOL_MIXED) {
+    if (is_v) put_value<D, FMT>(a, p, g, row, gl, act, v);
   }
 }
 
@@ -476,6 +533,9 @@ __device__ __forceinline__ float2 scale_zero(const uint8_t* p) {
                      __half2float(__ushort_as_half(static_cast<unsigned short>(sz >> 16))));
 }
 
+// c < 2^23 as a float, exactly, off the conversion pipe.
+__device__ __forceinline__ float small_float(uint32_t c) { return __uint_as_float(c | 0x4B000000u) - 8388608.f; }
+
 // Codes of `w` bits at bit `o` of a row of 32-bit words.
 __device__ __forceinline__ uint32_t get_bits(const uint32_t* row, int o, int w) {
   if (w == 0) return 0u;
@@ -496,7 +556,7 @@ __device__ __forceinline__ void read_vbf(const uint8_t* vblock, int r, int gl, f
 template <int D>
 __device__ __forceinline__ const uint8_t* slice_of(const AppendArgs& a, const Place& p, int g, int KR, int VR) {
   return a.pool + static_cast<size_t>(p.page) * a.page_bytes + static_cast<size_t>(g) * static_cast<size_t>(a.P) * (KR + VR + 8) +
-         static_cast<size_t>((p.pos % a.P) >> 4) * 16 * (KR + VR + 8);
+         static_cast<size_t>(in_page(a, p.pos) >> 4) * 16 * (KR + VR + 8);
 }
 
 // Key of one (token, KV head) as fp32 in its original basis, by its lane group.
@@ -524,7 +584,7 @@ __device__ __forceinline__ void read_key(const AppendArgs& a, const Place& p, in
     for (int j = 0; j < 8; ++j) {
       const uint32_t c = get_bits(src, o, w[j]);
       o += w[j];
-      const float mid = __fadd_rn(static_cast<float>(2u * c + 1u) * (1.f / static_cast<float>(1 << w[j])), -1.f);
+      const float mid = __fadd_rn(small_float(2u * c + 1u) * (1.f / static_cast<float>(1 << w[j])), -1.f);
       x[j] = w[j] ? __fmul_rn(__fmul_rn(ks, sig[(8 * gl + j) % (D / 2)]), mid) : 0.f;
     }
   } else if (FMT != POOL_BF16 && row >= 0) {
@@ -540,10 +600,14 @@ __device__ __forceinline__ void read_key(const AppendArgs& a, const Place& p, in
       load8(kbf_unit<D>(tile, r, 2 * gl), KV4_BF16, 0, x);
     } else {
       const float2 sz = scale_zero(tile + (FMT == POOL_VBF ? 8 * D : 16 * D) + 4 * r);
-      const unsigned long long w = *k4_group<D>(tile, r & 7, gl) >> (4 * (r >> 3));
+      const uint2 w = *reinterpret_cast<const uint2*>(k4_group<D>(tile, r & 7, gl));
+      const int sh = 4 * (r >> 3);
+      const uint32_t even = w.x >> sh, odd = w.y >> sh;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        x[j] = fmaf(sz.x, static_cast<float>(static_cast<uint32_t>(w >> (32 * (j & 1) + 8 * (j >> 1))) & 15u), sz.y);
+      for (int j = 0; j < 4; ++j) {
+        x[2 * j] = fmaf(sz.x, small_float((even >> (8 * j)) & 15u), sz.y);
+        x[2 * j + 1] = fmaf(sz.x, small_float((odd >> (8 * j)) & 15u), sz.y);
+      }
       unrotate8(a, gl, x);
     }
   }
@@ -559,7 +623,7 @@ __device__ __forceinline__ void read_value(const AppendArgs& a, const Place& p, 
     const float step = __fdiv_rn(zr.y, static_cast<float>((1 << a.vbits) - 1));
     const uint32_t* src = reinterpret_cast<const uint32_t*>(slice + 16 * static_cast<size_t>(KR) + static_cast<size_t>(r) * VR);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = fmaf(step, static_cast<float>(get_bits(src, (8 * gl + j) * a.vbits, a.vbits)), zr.x);
+    for (int j = 0; j < 8; ++j) x[j] = fmaf(step, small_float(get_bits(src, (8 * gl + j) * a.vbits, a.vbits)), zr.x);
   } else if (FMT != POOL_BF16 && row >= 0) {
     uint8_t* t8 = side_tile_of<D, FMT>(a, p.b, g, row);
     if constexpr (FMT == POOL_VBF) {
@@ -580,7 +644,7 @@ __device__ __forceinline__ void read_value(const AppendArgs& a, const Place& p, 
       const float2 sz = scale_zero(tile + 16 * D + 64 + 4 * r);
       const uint32_t c = *v4_chunk<D>(tile, r, 2 * gl) | (static_cast<uint32_t>(*v4_chunk<D>(tile, r, 2 * gl + 1)) << 16);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = fmaf(sz.x, static_cast<float>((c >> (4 * j)) & 15u), sz.y);
+      for (int j = 0; j < 8; ++j) x[j] = fmaf(sz.x, small_float((c >> (4 * j)) & 15u), sz.y);
     }
   }
   if (FMT == POOL_INT4 && a.rotate_v) unrotate8(a, gl, x);
@@ -618,10 +682,13 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(AppendArgs a, void* k_
 
 unsigned blocks_for(long long warps) { return static_cast<unsigned>((warps + kWarpsPerBlock - 1) / kWarpsPerBlock); }
 
-// Query heads a warp takes: one pass while the launch has fewer warps than the GPU holds (the latency
-// counts), kBatch passes' loads in flight otherwise.
+// Few vectors: the launch has fewer warps than the GPU holds and the latency counts.
 template <int D>
-int heads_per_warp(long long vectors) { return vectors > 148LL * 64 * kPerWarp<D> ? 2 * kBatch * kPerWarp<D> : kPerWarp<D>; }
+bool few(long long vectors) { return vectors <= 148LL * 64 * kPerWarp<D>; }
+
+// Query heads a warp takes: one pass when there are few, kBatch passes otherwise.
+template <int D>
+int heads_per_warp(long long vectors) { return few<D>(vectors) ? kPerWarp<D> : kBatch * kPerWarp<D>; }
 
 }  // namespace
 
@@ -633,7 +700,9 @@ cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t st) {
 }
 
 template <int D>
-static void launch_rope_d(const RopeArgs& a, cudaStream_t st) {
+static void launch_rope_d(RopeArgs a, cudaStream_t st) {
+  a.q_fast = rows16(a.q, a.q_dtype, a.q_stride, a.q_out, a.q_out_dtype, a.q_out_stride);
+  a.k_fast = rows16(a.k, a.k_dtype, a.k_stride, a.k_out, a.k_out_dtype, a.k_out_stride);
   const int hpw = heads_per_warp<D>(static_cast<long long>(a.T) * (a.Hq + a.Hkv));
   const unsigned grid = blocks_for(static_cast<long long>(a.T) * ((a.Hq + hpw - 1) / hpw + (a.Hkv + hpw - 1) / hpw));
   rope_kernel<D><<<grid, kThreads, 0, st>>>(a, hpw);
@@ -647,16 +716,19 @@ cudaError_t launch_rope(const RopeArgs& a, int D, cudaStream_t st) {
 }
 
 template <int D>
-static cudaError_t launch_append_rope_d(const RopeArgs& q, const AppendArgs& a, int format, cudaStream_t st) {
-  const int hpw = heads_per_warp<D>(static_cast<long long>(a.T) * (q.Hq + 2 * a.Hkv));
-  const int per = (q.Hq + hpw - 1) / hpw + (format == POOL_MIXED ? a.Hkv : 2 * ((a.Hkv + kPerWarp<D> - 1) / kPerWarp<D>));
+static cudaError_t launch_append_rope_d(RopeArgs q, const AppendArgs& a, int format, cudaStream_t st) {
+  q.q_fast = rows16(q.q, q.q_dtype, q.q_stride, q.q_out, q.q_out_dtype, q.q_out_stride);
+  const long long vectors = static_cast<long long>(a.T) * (q.Hq + 2 * a.Hkv);
+  const int hpw = heads_per_warp<D>(vectors), passes = (a.Hkv + kPerWarp<D> - 1) / kPerWarp<D>;
+  const bool joint = !few<D>(vectors);
+  const int per = (q.Hq + hpw - 1) / hpw + (format == POOL_MIXED ? a.Hkv : joint ? passes : 2 * passes);
   const unsigned grid = blocks_for(static_cast<long long>(a.T) * per);
   note_launches(1);
   switch (format) {
-    case POOL_INT4: append_rope_kernel<D, POOL_INT4><<<grid, kThreads, 0, st>>>(q, a, hpw); break;
-    case POOL_VBF: append_rope_kernel<D, POOL_VBF><<<grid, kThreads, 0, st>>>(q, a, hpw); break;
-    case POOL_MIXED: append_rope_kernel<D, POOL_MIXED><<<grid, kThreads, 0, st>>>(q, a, hpw); break;
-    default: append_rope_kernel<D, POOL_BF16><<<grid, kThreads, 0, st>>>(q, a, hpw); break;
+    case POOL_INT4: append_rope_kernel<D, POOL_INT4><<<grid, kThreads, 0, st>>>(q, a, hpw, joint); break;
+    case POOL_VBF: append_rope_kernel<D, POOL_VBF><<<grid, kThreads, 0, st>>>(q, a, hpw, joint); break;
+    case POOL_MIXED: append_rope_kernel<D, POOL_MIXED><<<grid, kThreads, 0, st>>>(q, a, hpw, joint); break;
+    default: append_rope_kernel<D, POOL_BF16><<<grid, kThreads, 0, st>>>(q, a, hpw, joint); break;
   }
   return cudaGetLastError();
 }
