@@ -187,6 +187,7 @@ struct Rotation {
       for (int j = 0; j < 8; ++j) o[j] = __shfl_sync(FULL, x[j ^ 4], j < 4 ? src_lo : src_hi);
     }
     if (on) {
+      // (as packed pairs the products and the sum were fused, against their .rn)
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = __fadd_rn(__fmul_rn(x[j], c[j]), __fmul_rn(o[j], s[j]));
     }
@@ -199,13 +200,14 @@ template <int D>
 __device__ __forceinline__ void head_norm(float (&x)[8], const float (&w)[8], float eps) {
   float s[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) s[j] = __fmul_rn(x[j], x[j]);
+  for (int j = 0; j < 8; j += 2) unpack2(mul2(pack2(x[j], x[j + 1]), pack2(x[j], x[j + 1])), s[j], s[j + 1]);
   float ss = __fadd_rn(__fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3])), __fadd_rn(__fadd_rn(s[4], s[5]), __fadd_rn(s[6], s[7])));
 #pragma unroll
   for (int o = 1; o < kLanes<D>; o <<= 1) ss = __fadd_rn(ss, __shfl_xor_sync(FULL, ss, o));
   const float r = __frsqrt_rn(__fadd_rn(__fmul_rn(ss, 1.0f / D), eps));
+  const uint64_t r2 = pack2(r, r);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(__fmul_rn(x[j], r), w[j]);
+  for (int j = 0; j < 8; j += 2) unpack2(mul2(mul2(pack2(x[j], x[j + 1]), r2), pack2(w[j], w[j + 1])), x[j], x[j + 1]);
 }
 
 template <int D>
@@ -686,9 +688,9 @@ unsigned blocks_for(long long warps) { return static_cast<unsigned>((warps + kWa
 template <int D>
 bool few(long long vectors) { return vectors <= 148LL * 64 * kPerWarp<D>; }
 
-// Query heads a warp takes: one pass when there are few, kBatch passes otherwise.
+// Heads a warp takes: one pass when there are few, two batches of passes otherwise.
 template <int D>
-int heads_per_warp(long long vectors) { return few<D>(vectors) ? kPerWarp<D> : kBatch * kPerWarp<D>; }
+int heads_per_warp(long long vectors) { return few<D>(vectors) ? kPerWarp<D> : 2 * kBatch * kPerWarp<D>; }
 
 }  // namespace
 

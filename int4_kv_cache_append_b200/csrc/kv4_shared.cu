@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
         bool slow = odd;
         if (!odd) {
           const float2 sz = sm.ksz[st][pos];
-          const uint64_t ks2 = tc::pack2(sz.x, sz.x), kz2 = tc::pack2(sz.y, sz.y);
+          const uint64_t ks2 = pack2(sz.x, sz.x), kz2 = pack2(sz.y, sz.y);
           const uint32_t scores = tm + quad + C::S + kRB * bf + 8 * wg;
           const float4* cst = &sm.cst[4 * wg];
           __half* pb = &sm.P[bf][wg * (kTile * 8) + pos * 8];
@@ -681,13 +681,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
             for (int j = 4 * k; j < 4 * k + 4; ++j) {
               // logits minus the running maximum, two rows at once
               const float4 cc = cst[4 * kSoftGroups * k + j - 4 * k];
-              const uint64_t sv = tc::pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-              const uint64_t x = tc::fma2(ks2, sv, tc::fma2(kz2, tc::pack2(cc.x, cc.y), tc::pack2(cc.z, cc.w)));
+              const uint64_t sv = pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+              const uint64_t x = fma2(ks2, sv, fma2(kz2, pack2(cc.x, cc.y), pack2(cc.z, cc.w)));
               float e0, e1;
-              tc::unpack2(x, e0, e1);
+              unpack2(x, e0, e1);
               top = tc::max3(top, e0, e1);
               const float x0 = exp2_fast(e0), x1 = exp2_fast(e1);
-              x2[j] = tc::pack2(x0, x1);
+              x2[j] = pack2(x0, x1);
               asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[j - 4 * k]) : "f"(x1), "f"(x0));
             }
             *reinterpret_cast<uint4*>(pb + k * (kSoftGroups * kTile * 8)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
@@ -698,17 +698,17 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
             for (int k = 0; k < kChunks; ++k) {
               if (k >= nch) break;
 #pragma unroll
-              for (int j = 4 * k; j < 4 * k + 4; ++j) l2[j] = tc::add2(l2[j], x2[j]);
+              for (int j = 4 * k; j < 4 * k + 4; ++j) l2[j] = add2(l2[j], x2[j]);
             }
           }
         }
         if (unlikely(slow)) {
           float l[8 * kChunks];
 #pragma unroll
-          for (int j = 0; j < 4 * kChunks; ++j) tc::unpack2(l2[j], l[2 * j], l[2 * j + 1]);
+          for (int j = 0; j < 4 * kChunks; ++j) unpack2(l2[j], l[2 * j], l[2 * j + 1]);
           soft_unit_slow<D>(sm, SoftUnit{tm + quad, wg, w4, lane, nch, p0, i, i == i0, !odd || i == i0}, sinks, l, a.err, a.wait_ns);
 #pragma unroll
-          for (int j = 0; j < 4 * kChunks; ++j) l2[j] = tc::pack2(l[2 * j], l[2 * j + 1]);
+          for (int j = 0; j < 4 * kChunks; ++j) l2[j] = pack2(l[2 * j], l[2 * j + 1]);
         }
         fence_proxy_async_smem();
         tc::fence_before();
@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
       // sums over the 128 positions: lanes j and j + 16 of each warp end with this group's column j
       float l[8 * kChunks];
 #pragma unroll
-      for (int j = 0; j < 4 * kChunks; ++j) tc::unpack2(l2[j], l[2 * j], l[2 * j + 1]);
+      for (int j = 0; j < 4 * kChunks; ++j) unpack2(l2[j], l[2 * j], l[2 * j + 1]);
       static_assert(8 * kChunks == 16, "two halves of a warp");
 #pragma unroll
       for (int j = 0; j < 16; ++j) l[j] += __shfl_xor_sync(FULL, l[j], 16);

@@ -140,6 +140,8 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+# A call's checks are a large part of a small call's time: sizes and strides are read once, devices as
+# integers, and the current stream as a raw handle where torch offers it.
 def _rows(t, what: str):
     """(pointer, kv4_dtype, elements between tokens) of a [T][heads][D] tensor whose heads are
     contiguous in a token; (None, 0, 0) for None."""
@@ -147,30 +149,39 @@ def _rows(t, what: str):
         return None, 0, 0
     if not t.is_cuda or t.dim() != 3:
         raise ValueError(f"{what}: device tensor [T][heads][D] expected")
-    T, H, D = t.shape
-    if t.dtype not in _DTYPES:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
         raise ValueError(f"{what}: float32, bfloat16 or float16 expected, got {t.dtype}")
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
-    return t.data_ptr(), _DTYPES[t.dtype], (t.stride(0) if T > 1 else H * D)
+    return t.data_ptr(), code, st if T > 1 else H * D
 
 
 def _i32(t, what: str):
-    if t is not None and t.dtype != torch.int32:
-        raise ValueError(f"{what}: int32 tensor expected, got {t.dtype}")
-    return _ptr(t)
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous int32 device tensor expected, got {t.dtype} on {t.device}")
+    return t.data_ptr()
 
 
 def _on_current_device(*tensors) -> None:
     """The library launches on the current device."""
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.device.index != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -308,12 +319,12 @@ def kv4_rope(params: kv4_rope_params, q, k, pos, q_out, k_out, stream=None):
             raise ValueError(f"{what}: the shape of its input expected")
     if q is not None and k is not None and (q.shape[0], q.shape[2]) != (k.shape[0], k.shape[2]):
         raise ValueError("q and k differ in tokens or head size")
-    T, D = int(x.shape[0]), int(x.shape[2])
+    T, _, D = x.shape
     if pos.numel() != T:
         raise ValueError("pos: one position per token expected")
     _on_current_device(q, k, pos, q_out, k_out)
-    _check("kv4_rope", lib.kv4_rope(ctypes.byref(params), T, q.shape[1] if q is not None else 0,
-                                    k.shape[1] if k is not None else 0, D, *_rows(q, "q"), *_rows(k, "k"),
+    _check("kv4_rope", lib.kv4_rope(ctypes.byref(params), T, q.size(1) if q is not None else 0,
+                                    k.size(1) if k is not None else 0, D, *_rows(q, "q"), *_rows(k, "k"),
                                     _i32(pos, "pos"), *_rows(q_out, "q_out"), *_rows(k_out, "k_out"), _stream(stream)))
 
 
@@ -323,8 +334,8 @@ def kv4_append_rope(handle, layer, params: kv4_rope_params, q, K, V, seq_slot, p
     normed and rotated queries (q and q_out None: append only)."""
     if (q is None) != (q_out is None) or (q is not None and q.shape != q_out.shape):
         raise ValueError("q_out: the shape of q expected")
-    T = int(seq_slot.numel())
-    if pos.numel() != T or any(x is not None and x.shape[0] != T for x in (q, K, V)) or K.shape != V.shape:
+    T = seq_slot.numel()
+    if pos.numel() != T or K.size(0) != T or K.shape != V.shape or (q is not None and q.size(0) != T):
         raise ValueError("q, K, V, seq_slot and pos must have the same tokens")
     _on_current_device(q, K, V, seq_slot, pos, lens_after, page_table, q_out)
     _check("kv4_append_rope", lib.kv4_append_rope(handle, layer, T, ctypes.byref(params), *_rows(q, "q"), *_rows(K, "K"),
@@ -484,9 +495,9 @@ class Rope:
 
     def apply(self, q, k, pos, q_out=None, k_out=None, stream=None):
         """Normed and rotated (q, k); new tensors of the inputs' types unless outputs are given."""
-        for x in (q, k):
-            if x is not None:
-                self.check_head_dim(int(x.shape[-1]))
+        x = q if q is not None else k
+        if x is not None:
+            self.check_head_dim(x.shape[-1])
         if q is not None and q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if k is not None and k_out is None:
@@ -503,25 +514,26 @@ class _RopeCacheMixin:
         queries (None when q is None).  lens_after is not read by a BF16 or mixed-key cache."""
         g = self.geo
         rope.check_head_dim(g.head_dim)
-        if tuple(K.shape[1:]) != (g.num_kv_heads, g.head_dim) or (q is not None and tuple(q.shape[1:]) != (g.num_q_heads, g.head_dim)):
+        if K.dim() != 3 or K.size(1) != g.num_kv_heads or K.size(2) != g.head_dim or (
+                q is not None and (q.dim() != 3 or q.size(1) != g.num_q_heads or q.size(2) != g.head_dim)):
             raise ValueError("q [T][Hq][D] and K, V [T][Hkv][D] of the cache's geometry expected")
         if q is not None and q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         kv4_append_rope(self.handle, layer, rope.params, q, K, V, seq_slot, pos, lens_after, page_table,
-                        int(page_table.shape[1]), q_out, stream)
+                        page_table.size(1), q_out, stream)
         return q_out
 
     def gather(self, layer, seq_slot, pos, page_table, lens=None, dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
         """Cached positions as dense (K, V) [T][Hkv][D] in their original basis."""
-        T = int(seq_slot.numel())
+        T = seq_slot.numel()
         if pos.numel() != T:
             raise ValueError("one position per seq_slot expected")
         shape = (T, self.geo.num_kv_heads, self.geo.head_dim)
         k_out = torch.empty(shape, dtype=dtype, device=pos.device) if k_out is None else k_out
         v_out = torch.empty(shape, dtype=dtype, device=pos.device) if v_out is None else v_out
-        if tuple(k_out.shape) != shape or tuple(v_out.shape) != shape or k_out.dtype != v_out.dtype:
+        if k_out.shape != shape or v_out.shape != shape or k_out.dtype != v_out.dtype:
             raise ValueError("k_out and v_out [T][Hkv][D] of one type expected")
-        kv4_gather(self.handle, layer, T, seq_slot, pos, lens, page_table, int(page_table.shape[1]), k_out, v_out,
+        kv4_gather(self.handle, layer, T, seq_slot, pos, lens, page_table, page_table.size(1), k_out, v_out,
                    dtype_code(k_out), stream)
         return k_out, v_out
 
@@ -588,19 +600,19 @@ class Cache(_RopeCacheMixin):
                       workspace=None, stream=None):
         """Decode of a batch whose row groups [group_start[i], group_start[i + 1]) share their first
         prefix_len[i] positions; out has q's type unless given."""
-        B, n = int(lens.numel()), int(prefix_len.numel())
+        B, n = lens.numel(), prefix_len.numel()
         shape = (B, self.geo.num_q_heads, self.geo.head_dim)
-        if tuple(q.shape) != shape or page_table.shape[0] < B:
+        if q.shape != shape or page_table.size(0) < B:
             raise ValueError("q [B][Hq][D] and a page-table row per sequence expected")
         if group_start.numel() != n + 1:
             raise ValueError("group_start: one entry more than prefix_len expected")
         if out is None:
             out = torch.empty(shape, dtype=q.dtype, device=q.device)
-        elif tuple(out.shape) != shape:
+        elif out.shape != shape:
             raise ValueError("out [B][Hq][D] expected")
         if workspace is None:
             workspace = self.shared_workspace(B, n)
-        kv4_decode_attn_shared(self.handle, layer, B, q, dtype_code(q), page_table, int(page_table.shape[1]), lens, n,
+        kv4_decode_attn_shared(self.handle, layer, B, q, dtype_code(q), page_table, page_table.size(1), lens, n,
                                group_start, prefix_len, max_len_hint, out, dtype_code(out), lse, workspace,
                                workspace.numel(), stream)
         return out
