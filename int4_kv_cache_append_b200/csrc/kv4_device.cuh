@@ -195,4 +195,12 @@ __device__ __forceinline__ uint32_t pack_bf2(__nv_bfloat16 lo, __nv_bfloat16 hi)
   return static_cast<uint32_t>(__bfloat16_as_ushort(lo)) | (static_cast<uint32_t>(__bfloat16_as_ushort(hi)) << 16);
 }
 
+// Two fp32 values to a bf16 pair (nearest even) by one instruction; one at a time they go through the
+// conversion pipe, which is a quarter as wide.
+__device__ __forceinline__ uint32_t pack_bf2_rn(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
 }  // namespace kv4

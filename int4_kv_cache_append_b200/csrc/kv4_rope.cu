@@ -68,7 +68,7 @@ __device__ __forceinline__ void store8(void* base, int dtype, long long i, const
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (dtype == KV4_BF16) {
-      w[j] = pack_bf2(__float2bfloat16_rn(x[2 * j]), __float2bfloat16_rn(x[2 * j + 1]));
+      w[j] = pack_bf2_rn(x[2 * j], x[2 * j + 1]);
     } else {
       const __half2 h = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
       w[j] = *reinterpret_cast<const uint32_t*>(&h);
@@ -237,7 +237,7 @@ __device__ __forceinline__ uint4 narrow8(const float (&x)[8], bool bf16) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (bf16) {
-      w[j] = pack_bf2(__float2bfloat16_rn(x[2 * j]), __float2bfloat16_rn(x[2 * j + 1]));
+      w[j] = pack_bf2_rn(x[2 * j], x[2 * j + 1]);
     } else {
       const __half2 h = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
       w[j] = *reinterpret_cast<const uint32_t*>(&h);
@@ -380,10 +380,10 @@ __device__ __forceinline__ void put_key(const AppendArgs& a, const Place& p, int
     if (act) {
       // both 4-element halves of the lane are in one 16-byte unit
       uint4 w;
-      w.x = pack_bf2(__float2bfloat16_rn(k[0]), __float2bfloat16_rn(k[1]));
-      w.y = pack_bf2(__float2bfloat16_rn(k[2]), __float2bfloat16_rn(k[3]));
-      w.z = pack_bf2(__float2bfloat16_rn(k[4]), __float2bfloat16_rn(k[5]));
-      w.w = pack_bf2(__float2bfloat16_rn(k[6]), __float2bfloat16_rn(k[7]));
+      w.x = pack_bf2_rn(k[0], k[1]);
+      w.y = pack_bf2_rn(k[2], k[3]);
+      w.z = pack_bf2_rn(k[4], k[5]);
+      w.w = pack_bf2_rn(k[6], k[7]);
       *reinterpret_cast<uint4*>(kbf_unit<D>(tile, r, 2 * gl)) = w;
     }
   } else {
@@ -652,7 +652,8 @@ __device__ __forceinline__ void read_value(const AppendArgs& a, const Place& p, 
   if (FMT == POOL_INT4 && a.rotate_v) unrotate8(a, gl, x);
 }
 
-// Warp (token, kPerWarp KV heads).
+// Warp (token, kPerWarp KV heads).  One pass a warp at any size: four in a loop saved a fifth of the
+// instructions but took 64 registers instead of 40, and the warps it cost were worth more (54 us for 43).
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads) gather_kernel(AppendArgs a, void* k_out, void* v_out, int dtype) {
   const int lane = threadIdx.x & 31, gl = lane % kLanes<D>;
