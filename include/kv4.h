@@ -251,8 +251,10 @@ kv4_status kv4_set_decode_overlap(kv4_cache* cache, int enable);
  * undefined; the context stays usable, and a call with 0 decodes normally.  The mixed
  * bit-width key cache takes the same path: each decode warp's first wait is on a barrier nothing
  * arrives on, runs out after 1 ms, sets KV4_DEVERR_WAIT_LIMIT, and the warp waits (bounded) for
- * its copies in flight and returns; that call's out and lse are undefined.  Returns
- * KV4_ERR_INVALID_ARG for a NULL or BF16 cache.
+ * its copies in flight and returns; that call's out and lse are undefined.  So does
+ * kv4_decode_attn_shared: the softmax warps of its prefix kernel start with such a wait, after
+ * which every warp of the block runs its loop to the end without waiting, and its other two
+ * kernels are those of kv4_decode_attn.  Returns KV4_ERR_INVALID_ARG for a NULL or BF16 cache.
  */
 kv4_status kv4_debug_force_wait_timeout(kv4_cache* cache, int enable);
 
@@ -314,8 +316,9 @@ kv4_status kv4_bf16_decode_attn(kv4_cache* cache, int layer, int B, const void* 
  * [n_groups + 1], non-decreasing, within [0, B]; rows before the first and after the last group
  * share nothing), and the first prefix_len[i] positions (device int32 [n_groups]) of its sequences
  * lie in pages with the same contents; they are read through the page-table row of the group's
- * first sequence, whole 16 positions at a time (what is left of prefix_len past a multiple of 16
- * is read as each sequence's own).  The page ids of the other rows may be the same (pages shared)
+ * first sequence, which therefore lists pages for the whole prefix even where that sequence is
+ * shorter, whole 16 positions at a time (what is left of prefix_len past a multiple of 16 is read
+ * as each sequence's own).  The page ids of the other rows may be the same (pages shared)
  * or not (copies).  A prefix may be longer than some of its sequences; each attends what it would
  * in kv4_decode_attn: its own INT8 sink and recent rows, and the INT4 positions before its recent
  * window.  Attention of the INT4 cache with INT4 values (KV4_ERR_UNSUPPORTED for KV4_VALUES_BF16,

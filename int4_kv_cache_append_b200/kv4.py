@@ -484,11 +484,12 @@ class Rope:
 
     def build(self, stream=None) -> torch.Tensor:
         """(Re)write the table on the stream; other streams must wait for it."""
-        _on_current_device(self.table)
+        _on_current_device(self.table, self.q_weight, self.k_weight)
         kv4_rope_table(self.cfg, self.table, stream)
         return self.table
 
     def check_head_dim(self, D: int) -> None:
+        _on_current_device(self.table)
         for w in (self.q_weight, self.k_weight):
             if w is not None and w.numel() != D:
                 raise ValueError(f"norm weights of {w.numel()} elements for heads of {D}")
@@ -610,8 +611,12 @@ class Cache(_RopeCacheMixin):
             out = torch.empty(shape, dtype=q.dtype, device=q.device)
         elif out.shape != shape:
             raise ValueError("out [B][Hq][D] expected")
+        if lse is not None and (lse.shape != shape[:2] or lse.dtype is not torch.float32):
+            raise ValueError("lse float32 [B][Hq] expected")
         if workspace is None:
             workspace = self.shared_workspace(B, n)
+        elif workspace.dtype is not torch.uint8:
+            raise ValueError("workspace: uint8 tensor expected")
         kv4_decode_attn_shared(self.handle, layer, B, q, dtype_code(q), page_table, page_table.size(1), lens, n,
                                group_start, prefix_len, max_len_hint, out, dtype_code(out), lse, workspace,
                                workspace.numel(), stream)

@@ -382,3 +382,18 @@ def test_python_checks(kv4):
         rope.apply(q, None, i32([0]))
     with pytest.raises(ValueError):
         rope.apply(q.double(), None, i32([0, 1]))
+    with pytest.raises(ValueError):
+        kv4.Rope(kv4.RopeGeometry(64, 16), torch.ones(64))  # weights on the host
+
+
+def test_gather_of_repeated_and_no_positions(kv4):
+    wl = W.make_workload("twice", 3, 1, 2, 8, 2, 128, 16, 4, 16, 128, lambda _: [40, 21], W.F32, W.F32, W.F32, 2, 6.0)
+    cache = T.gpu_cache_from_host_inputs(wl)
+    pt, lens = torch.from_numpy(wl.page_table).cuda(), torch.from_numpy(wl.lens).cuda()
+    b, p = T.prefill_tokens(wl.lens)
+    k, v = cache.gather(0, i32(b), i32(p), pt, lens)
+    pick = np.array([0, 60, 0, 0, 39, 60])
+    k2, v2 = cache.gather(0, i32(b[pick]), i32(p[pick]), pt, lens)
+    assert torch.equal(k2, k[pick]) and torch.equal(v2, v[pick])
+    k0, v0 = cache.gather(0, i32([]), i32([]), pt, lens)
+    assert k0.shape == v0.shape == (0, 2, 128)

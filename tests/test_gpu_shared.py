@@ -349,3 +349,52 @@ def test_values_beyond_fp16(kv4):
     out = r.cache.decode_shared(0, r.q, r.pt, r.lens, r.start_d, r.prefix_d, out=torch.empty(r.q.shape, device="cuda"))
     assert np.isfinite(want[0]).all() and want[2].max() < 1e5
     check(r, out, None, want)
+
+
+@gpu
+@pytest.mark.parametrize("name", ["ragged", "b300", "long"])
+def test_wait_limit_failure_path_reports_and_recovers(kv4, name):
+    """The bounded waits made to run out by the test hook: the error bit is set, the kernels end, the
+    context stays usable and the next call is right."""
+    r = build(CASES[IDS.index(name)], kv4)
+    want = reference(r)
+    n = kv4.kv4_decode_shared_workspace_bytes(r.cache.handle, r.wl.B, len(r.prefix))
+    ws = torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
+    kv4.kv4_debug_force_wait_timeout(r.cache.handle, True)
+    try:
+        r.cache.decode_shared(0, r.q, r.pt, r.lens, r.start_d, r.prefix_d, workspace=ws)
+        torch.cuda.synchronize()
+    finally:
+        kv4.kv4_debug_force_wait_timeout(r.cache.handle, False)
+    assert kv4.kv4_get_device_error() & kv4.KV4_DEVERR_WAIT_LIMIT
+    lse = torch.empty((r.wl.B, r.wl.Hq), device="cuda")
+    out = r.cache.decode_shared(0, r.q, r.pt, r.lens, r.start_d, r.prefix_d, lse=lse, workspace=ws)
+    check(r, out, lse, want, 2.0 ** -8)
+    assert kv4.kv4_get_device_error() == 0
+
+
+@gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_query_stays_in_its_row(kv4, bad):
+    r = build(CASES[IDS.index("many-rows")], kv4)
+    want = r.cache.decode_shared(0, r.q, r.pt, r.lens, r.start_d, r.prefix_d)
+    q = r.q.clone()
+    q[3, 1] = bad
+    got = r.cache.decode_shared(0, q, r.pt, r.lens, r.start_d, r.prefix_d)
+    other = torch.ones(q.shape[:2], dtype=torch.bool, device="cuda")
+    other[3, 1] = False
+    assert torch.equal(got[other], want[other])
+
+
+@gpu
+def test_python_checks(kv4):
+    r = build(CASES[0], kv4)
+    call = lambda **kw: r.cache.decode_shared(0, r.q, r.pt, r.lens, r.start_d, r.prefix_d, **kw)  # noqa: E731
+    for kw in (dict(lse=torch.empty(r.wl.B, 1, device="cuda")), dict(lse=torch.empty(r.wl.B, r.wl.Hq, dtype=torch.float64, device="cuda")),
+               dict(out=torch.empty(r.wl.B, r.wl.Hq, 1, device="cuda")), dict(workspace=torch.empty(1 << 20, device="cuda"))):
+        with pytest.raises(ValueError):
+            call(**kw)
+    with pytest.raises(ValueError):
+        r.cache.decode_shared(0, r.q.transpose(0, 1).contiguous().transpose(0, 1), r.pt, r.lens, r.start_d, r.prefix_d)
+    with pytest.raises(ValueError):
+        r.cache.decode_shared(0, r.q, r.pt, r.lens, r.start_d[:1], r.prefix_d)
