@@ -9,7 +9,7 @@
 // Every step is a single fp32 operation in a fixed order (no contraction; the sum of squares is a
 // binary tree over the elements, the root IEEE-rounded), so that the codes an append writes do not
 // depend on the launch.  A sum in fp64 was 550 cycles of dependent latency a vector and the kernel's
-// bound.  The rotated key enters the cache's encoder in fp32: it is rounded to no 16-bit type on the way.
+// bound (160 us for what the tree does in 131).  The rotated key enters the cache's encoder in fp32: it is rounded to no 16-bit type on the way.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(RopeTableArgs a) {
 // ------------------------------------------------------------------ norm and rotation of one vector
 
 // D / 8 lanes hold one head vector, lane gl of the group elements 8 gl..8 gl + 7; a warp takes kPerWarp
-// vectors (heads of one token) at once.  Sixteen bytes a lane and half the shuffles of a vector
-// spread over the whole warp: the norm and rotation of 16383 tokens went from 206 us to 131.
+// vectors (heads of one token) at once: sixteen bytes a lane and half the shuffles of a vector spread
+// over the whole warp (the norm and rotation of 16383 tokens: 207 -> 160 us).
 template <int D>
 constexpr int kLanes = D / 8;
 template <int D>
@@ -252,11 +252,12 @@ __host__ __device__ inline bool rows16(const void* in, int in_dt, long long in_s
          ((in_stride | out_stride) & 7) == 0;
 }
 
-// Heads h0.. (below h1) of one token: norm, rotation, out.  fast (rows16): the loads of kBatch warp
-// passes of kPerWarp heads are issued before the first is worked on (64 bytes a lane in flight; one
-// pass at a time, the kernel waited on memory: 131 us instead of 90 for 16383 tokens).
-constexpr int kBatch = 4;
-template <int D>
+// Heads h0.. (below h1) of one token: norm, rotation, out.  fast (rows16): the loads of BATCH warp
+// passes of kPerWarp heads are issued before the first is worked on.  kv4_rope takes four (64 bytes a
+// lane in flight; 16383 tokens of 32 + 8 heads: 131 us with one, 111 with four).  The append takes
+// two, for its registers.
+constexpr int kRunPasses = 8;  // passes of a warp when there are many heads
+template <int D, int BATCH>
 __device__ __forceinline__ void rope_heads(const RopeArgs& a, const Rotation<D>& rot, const float (&w)[8], bool norm, const void* in,
                                            int in_dt, long long i0, void* out, int out_dt, long long o0, int h0, int h1, bool fast, int lane) {
   const int mine = lane / kLanes<D>, e = 8 * (lane % kLanes<D>);
@@ -264,15 +265,15 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a, const Rotation<D>&
     const uint16_t* src = reinterpret_cast<const uint16_t*>(in) + i0 + e;
     uint16_t* dst = reinterpret_cast<uint16_t*>(out) + o0 + e;
     const bool bi = in_dt == KV4_BF16, bo = out_dt == KV4_BF16;
-    for (int h = h0 + mine; h - mine < h1; h += kBatch * kPerWarp<D>) {
-      uint4 raw[kBatch];
+    for (int h = h0 + mine; h - mine < h1; h += BATCH * kPerWarp<D>) {
+      uint4 raw[BATCH];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
+      for (int u = 0; u < BATCH; ++u) {
         const int k = h + u * kPerWarp<D>;
         raw[u] = k < h1 ? __ldcs(reinterpret_cast<const uint4*>(src + k * D)) : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
+      for (int u = 0; u < BATCH; ++u) {
         const int k = h + u * kPerWarp<D>;
         if (k - mine >= h1) break;
         float x[8];
@@ -298,9 +299,12 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a, const Rotation<D>&
 
 // ------------------------------------------------------------------ kv4_rope
 
-// Warp (token, run of hpw heads): queries first, then keys.
+// Warp (token, run of hpw heads): queries first, then keys.  Four blocks an SM (64 registers, a few
+// spilled) hide more of the loads' latency than three (80): 97 -> 92 us for 16383 tokens of 32 + 8
+// heads in bf16, 3.7 TB/s of the 6.55 a copy reaches.  What is left is latency and issue (2.7
+// instructions a cycle an SM): a norm's tree, its root and its products depend on one another.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 3) rope_kernel(RopeArgs a, int hpw) {
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(RopeArgs a, int hpw) {
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int nq = (a.Hq + hpw - 1) / hpw, nk = (a.Hkv + hpw - 1) / hpw;
@@ -319,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_kernel(RopeArgs a, int hpw) 
   rot.load(a, pos, lane);
   float w[8];
   load_weight<D>(weight, a.w_dtype, lane, w);
-  rope_heads<D>(a, rot, w, weight != nullptr, is_q ? a.q : a.k, is_q ? a.q_dtype : a.k_dtype, t * (is_q ? a.q_stride : a.k_stride),
+  rope_heads<D, 4>(a, rot, w, weight != nullptr, is_q ? a.q : a.k, is_q ? a.q_dtype : a.k_dtype, t * (is_q ? a.q_stride : a.k_stride),
                 is_q ? a.q_out : a.k_out, is_q ? a.q_out_dtype : a.k_out_dtype, t * (is_q ? a.q_out_stride : a.k_out_stride), h0, h1,
                 is_q ? a.q_fast : a.k_fast, lane);
 }
@@ -448,9 +452,11 @@ __device__ __forceinline__ void put_value(const AppendArgs& a, const Place& p, i
 // Warp (token, item): items are runs of hpw query heads, then passes of kPerWarp KV heads: the key and
 // the value of each together with `joint` (one prologue and both loads in flight; many tokens), else
 // keys and values apart (few tokens: the latency counts).  Mixed bit-width keys: one KV head an item,
-// key and value share a record.
+// key and value share a record.  Four blocks an SM, as in rope_kernel: an encoder is a chain of
+// shuffles, a division and the codes' packing, and more warps hide more of it (16383 tokens of 32 + 8
+// heads: 181 us with three, 161 with four, 175 with five and their spills; 2.3 instructions a cycle).
 template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads, 3) append_rope_kernel(RopeArgs q, AppendArgs a, int hpw, bool joint) {
+__global__ void __launch_bounds__(kThreads, 4) append_rope_kernel(RopeArgs q, AppendArgs a, int hpw, bool joint) {
   constexpr int NI = D / 32, HP = FMT == POOL_MIXED ? 1 : kPerWarp<D>;
   __shared__ uint32_t rows[FMT == POOL_MIXED ? kWarpsPerBlock : 1][2][kMixedRowWords<D>];
   __shared__ float xs[FMT == POOL_MIXED ? kWarpsPerBlock : 1][D];
@@ -471,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_rope_kernel(RopeArgs q, Ap
     float w[8];
     rot.load(q, p.pos, lane);
     load_weight<D>(q.qw, q.w_dtype, lane, w);
-    rope_heads<D>(q, rot, w, q.qw != nullptr, q.q, q.q_dtype, t * q.q_stride, q.q_out, q.q_out_dtype, t * q.q_out_stride, c * hpw,
+    rope_heads<D, 2>(q, rot, w, q.qw != nullptr, q.q, q.q_dtype, t * q.q_stride, q.q_out, q.q_out_dtype, t * q.q_out_stride, c * hpw,
                   min((c + 1) * hpw, q.Hq), q.q_fast, lane);
     return;
   }
@@ -652,10 +658,11 @@ __device__ __forceinline__ void read_value(const AppendArgs& a, const Place& p, 
   if (FMT == POOL_INT4 && a.rotate_v) unrotate8(a, gl, x);
 }
 
-// Warp (token, kPerWarp KV heads).  One pass a warp at any size: four in a loop saved a fifth of the
-// instructions but took 64 registers instead of 40, and the warps it cost were worth more (54 us for 43).
+// Warp (token, kPerWarp KV heads).  Bound by issue (2.9 instructions a cycle), so the warps in flight
+// count: eight blocks an SM (32 registers) read 16383 positions of 8 heads back in 38 us, 40 registers in
+// 41, and four passes a warp in a loop, a fifth of the instructions fewer but 64 registers, in 46.
 template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads) gather_kernel(AppendArgs a, void* k_out, void* v_out, int dtype) {
+__global__ void __launch_bounds__(kThreads, 8) gather_kernel(AppendArgs a, void* k_out, void* v_out, int dtype) {
   const int lane = threadIdx.x & 31, gl = lane % kLanes<D>;
   const int per = (a.Hkv + kPerWarp<D> - 1) / kPerWarp<D>;
   const int gw = static_cast<int>((blockIdx.x * static_cast<unsigned>(kThreads) + threadIdx.x) >> 5);
@@ -689,9 +696,9 @@ unsigned blocks_for(long long warps) { return static_cast<unsigned>((warps + kWa
 template <int D>
 bool few(long long vectors) { return vectors <= 148LL * 64 * kPerWarp<D>; }
 
-// Heads a warp takes: one pass when there are few, two batches of passes otherwise.
+// Heads a warp takes: one pass when there are few, kRunPasses otherwise (their table row and weights are read once).
 template <int D>
-int heads_per_warp(long long vectors) { return few<D>(vectors) ? kPerWarp<D> : 2 * kBatch * kPerWarp<D>; }
+int heads_per_warp(long long vectors) { return few<D>(vectors) ? kPerWarp<D> : kRunPasses * kPerWarp<D>; }
 
 }  // namespace
 
