@@ -144,7 +144,7 @@ def peaks():
 
 def decode_sources_digest() -> str:
     h = hashlib.sha256()
-    for f in ("kv4_decode.cu", "kv4_device.cuh", "kv4_layout.cuh"):
+    for f in ("kv4_decode.cu", "kv4_decode_kernel.cuh", "kv4_device.cuh", "kv4_layout.cuh"):
         h.update(open(os.path.join(ROOT, "int4_kv_cache_append_b200", "csrc", f), "rb").read())
     return h.hexdigest()[:16]
 

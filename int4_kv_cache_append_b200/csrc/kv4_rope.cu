@@ -9,7 +9,8 @@
 // Every step is a single fp32 operation in a fixed order (no contraction; the sum of squares is a
 // binary tree over the elements, the root IEEE-rounded), so that the codes an append writes do not
 // depend on the launch.  A sum in fp64 was 550 cycles of dependent latency a vector and the kernel's
-// bound (160 us for what the tree does in 131).  The rotated key enters the cache's encoder in fp32: it is rounded to no 16-bit type on the way.
+// bound (160 us for what the tree does in 131).  The rotated key enters the cache's encoder in fp32: it
+// is rounded to no 16-bit type on the way.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -453,8 +454,9 @@ __device__ __forceinline__ void put_value(const AppendArgs& a, const Place& p, i
 // the value of each together with `joint` (one prologue and both loads in flight; many tokens), else
 // keys and values apart (few tokens: the latency counts).  Mixed bit-width keys: one KV head an item,
 // key and value share a record.  Four blocks an SM, as in rope_kernel: an encoder is a chain of
-// shuffles, a division and the codes' packing, and more warps hide more of it (16383 tokens of 32 + 8
-// heads: 181 us with three, 161 with four, 175 with five and their spills; 2.3 instructions a cycle).
+// shuffles, a division and the codes' packing, and more warps hide more of it (14460 tokens of 32 + 8
+// heads: 181 us with three, 169 with four, 175 with five and their spills; 161 with four and two query
+// loads in flight instead of four; 2.3 instructions a cycle).
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads, 4) append_rope_kernel(RopeArgs q, AppendArgs a, int hpw, bool joint) {
   constexpr int NI = D / 32, HP = FMT == POOL_MIXED ? 1 : kPerWarp<D>;
@@ -659,7 +661,7 @@ __device__ __forceinline__ void read_value(const AppendArgs& a, const Place& p, 
 }
 
 // Warp (token, kPerWarp KV heads).  Bound by issue (2.9 instructions a cycle), so the warps in flight
-// count: eight blocks an SM (32 registers) read 16383 positions of 8 heads back in 38 us, 40 registers in
+// count: eight blocks an SM (32 registers) read 14460 positions of 8 heads back in 38 us, 40 registers in
 // 41, and four passes a warp in a loop, a fifth of the instructions fewer but 64 registers, in 46.
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads, 8) gather_kernel(AppendArgs a, void* k_out, void* v_out, int dtype) {
