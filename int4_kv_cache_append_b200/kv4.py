@@ -142,17 +142,15 @@ def _ptr(t) -> int | None:
 
 # A call's checks are a large part of a small call's time: sizes and strides are read once, devices as
 # integers, and the current stream as a raw handle where torch offers it.
-def _rows(t, what: str):
-    """(pointer, kv4_dtype, elements between tokens) of a [T][heads][D] tensor whose heads are
-    contiguous in a token; (None, 0, 0) for None."""
-    if t is None:
-        return None, 0, 0
-    if not t.is_cuda or t.dim() != 3:
+def _rows(t, shape, what: str):
+    """(pointer, kv4_dtype, elements between tokens) of a tensor of shape [T][heads][D] whose heads are
+    contiguous in a token."""
+    if not t.is_cuda or len(shape) != 3:
         raise ValueError(f"{what}: device tensor [T][heads][D] expected")
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"{what}: float32, bfloat16 or float16 expected, got {t.dtype}")
-    T, H, D = t.shape
+    T, H, D = shape
     st, sh, sd = t.stride()
     if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
@@ -311,37 +309,52 @@ def kv4_rope_table(cfg: kv4_rope_config, table, stream=None):
 
 def kv4_rope(params: kv4_rope_params, q, k, pos, q_out, k_out, stream=None):
     """Norm and rotate T tokens' queries [T][Hq][D] and keys [T][Hkv][D] (either may be None)."""
-    x = q if q is not None else k
-    if x is None:
+    if q is None and k is None:
         raise ValueError("q or k expected")
-    for src, dst, what in ((q, q_out, "q_out"), (k, k_out, "k_out")):
-        if (src is None) != (dst is None) or (src is not None and src.shape != dst.shape):
-            raise ValueError(f"{what}: the shape of its input expected")
-    if q is not None and k is not None and (q.shape[0], q.shape[2]) != (k.shape[0], k.shape[2]):
-        raise ValueError("q and k differ in tokens or head size")
-    T, _, D = x.shape
-    if pos.numel() != T:
+    rows, heads, tokens, size = [], [], None, None
+    for src, dst, what in ((q, q_out, "q"), (k, k_out, "k")):
+        if src is None:
+            if dst is not None:
+                raise ValueError(f"{what}_out without {what}")
+            rows += (None, 0, 0), (None, 0, 0)
+            heads.append(0)
+            continue
+        shape = src.shape
+        if dst is None or dst.shape != shape:
+            raise ValueError(f"{what}_out: the shape of its input expected")
+        rows += _rows(src, shape, what), _rows(dst, shape, what + "_out")
+        if tokens is not None and (tokens != shape[0] or size != shape[2]):
+            raise ValueError("q and k differ in tokens or head size")
+        tokens, _, size = shape
+        heads.append(shape[1])
+    if pos.numel() != tokens:
         raise ValueError("pos: one position per token expected")
     _on_current_device(q, k, pos, q_out, k_out)
-    _check("kv4_rope", lib.kv4_rope(ctypes.byref(params), T, q.size(1) if q is not None else 0,
-                                    k.size(1) if k is not None else 0, D, *_rows(q, "q"), *_rows(k, "k"),
-                                    _i32(pos, "pos"), *_rows(q_out, "q_out"), *_rows(k_out, "k_out"), _stream(stream)))
+    _check("kv4_rope", lib.kv4_rope(ctypes.byref(params), tokens, heads[0], heads[1], size, *rows[0], *rows[2],
+                                    _i32(pos, "pos"), *rows[1], *rows[3], _stream(stream)))
 
 
 def kv4_append_rope(handle, layer, params: kv4_rope_params, q, K, V, seq_slot, pos, lens_after, page_table, stride,
                     q_out, stream=None):
     """Append keys and values [T][Hkv][D], the keys normed and rotated on the way; q_out receives the
     normed and rotated queries (q and q_out None: append only)."""
-    if (q is None) != (q_out is None) or (q is not None and q.shape != q_out.shape):
-        raise ValueError("q_out: the shape of q expected")
-    T = seq_slot.numel()
-    if pos.numel() != T or K.size(0) != T or K.shape != V.shape or (q is not None and q.size(0) != T):
+    T, shape = seq_slot.numel(), K.shape
+    if q is None:
+        rq = ro = (None, 0, 0)
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        qs = q.shape
+        if q_out is None or q_out.shape != qs or qs[0] != T:
+            raise ValueError("q and q_out of one shape, with the tokens of seq_slot, expected")
+        rq, ro = _rows(q, qs, "q"), _rows(q_out, qs, "q_out")
+    if pos.numel() != T or shape[0] != T or shape != V.shape:
         raise ValueError("q, K, V, seq_slot and pos must have the same tokens")
     _on_current_device(q, K, V, seq_slot, pos, lens_after, page_table, q_out)
-    _check("kv4_append_rope", lib.kv4_append_rope(handle, layer, T, ctypes.byref(params), *_rows(q, "q"), *_rows(K, "K"),
-                                                  *_rows(V, "V"), _i32(seq_slot, "seq_slot"), _i32(pos, "pos"),
+    _check("kv4_append_rope", lib.kv4_append_rope(handle, layer, T, ctypes.byref(params), *rq, *_rows(K, shape, "K"),
+                                                  *_rows(V, shape, "V"), _i32(seq_slot, "seq_slot"), _i32(pos, "pos"),
                                                   _i32(lens_after, "lens_after"), _i32(page_table, "page_table"), stride,
-                                                  *_rows(q_out, "q_out"), _stream(stream)))
+                                                  *ro, _stream(stream)))
 
 
 def kv4_gather(handle, layer, T, seq_slot, pos, lens, page_table, stride, K_out, V_out, out_dtype, stream=None):
@@ -515,8 +528,7 @@ class _RopeCacheMixin:
         queries (None when q is None).  lens_after is not read by a BF16 or mixed-key cache."""
         g = self.geo
         rope.check_head_dim(g.head_dim)
-        if K.dim() != 3 or K.size(1) != g.num_kv_heads or K.size(2) != g.head_dim or (
-                q is not None and (q.dim() != 3 or q.size(1) != g.num_q_heads or q.size(2) != g.head_dim)):
+        if K.shape[1:] != (g.num_kv_heads, g.head_dim) or (q is not None and q.shape[1:] != (g.num_q_heads, g.head_dim)):
             raise ValueError("q [T][Hq][D] and K, V [T][Hkv][D] of the cache's geometry expected")
         if q is not None and q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
