@@ -231,13 +231,14 @@ kv4_status kv4_set_value_rotation(kv4_cache* cache, int enable);
 /*
  * kv4_set_decode_overlap: how kv4_decode_attn of this cache starts (default 0).  Its kernel is
  * always launched as a programmatic dependent of the preceding kernel on the stream, and the
- * append kernel lets its dependent launch early.  With 0 the decode kernel reads nothing before
- * the preceding kernel has completed: stream order exactly.  With 1 it builds its work schedule
- * and first copy descriptors, reading lens and page_table only, while the preceding kernel runs,
- * then waits for it before reading q or the cache or writing any output; lens and page_table
- * must then not be written by the kernel that immediately precedes the decode on the stream
- * (writes earlier in stream order are fine).  Returns KV4_ERR_INVALID_ARG for a NULL or BF16
- * cache.
+ * kernels of kv4_append, kv4_append_rope and kv4_rope let their dependent launch early.
+ * (kv4_decode_attn_shared keeps stream order exactly, whatever is set here.)  With 0 the decode
+ * kernel reads nothing before the preceding kernel has completed: stream order exactly.  With 1
+ * it builds its work schedule and first copy descriptors, reading lens and page_table only,
+ * while the preceding kernel runs, then waits for it before reading q or the cache or writing
+ * any output; lens and page_table must then not be written by the kernel that immediately
+ * precedes the decode on the stream (writes earlier in stream order are fine).  Returns
+ * KV4_ERR_INVALID_ARG for a NULL or BF16 cache.
  */
 kv4_status kv4_set_decode_overlap(kv4_cache* cache, int enable);
 
@@ -319,9 +320,11 @@ kv4_status kv4_bf16_decode_attn(kv4_cache* cache, int layer, int B, const void* 
  * first sequence, which therefore lists pages for the whole prefix even where that sequence is
  * shorter, whole 16 positions at a time (what is left of prefix_len past a multiple of 16 is read
  * as each sequence's own).  The page ids of the other rows may be the same (pages shared)
- * or not (copies).  A prefix may be longer than some of its sequences; each attends what it would
- * in kv4_decode_attn: its own INT8 sink and recent rows, and the INT4 positions before its recent
- * window.  Attention of the INT4 cache with INT4 values (KV4_ERR_UNSUPPORTED for KV4_VALUES_BF16,
+ * or not (copies); where a prompt ends inside a page that each sequence continues in a page of
+ * its own without a copy of the prompt's end, prefix_len counts the whole pages only.  A prefix
+ * may be longer than some of its sequences; each attends what it would in kv4_decode_attn: its
+ * own INT8 sink and recent rows, and the INT4 positions before its recent window.  Attention of
+ * the INT4 cache with INT4 values (KV4_ERR_UNSUPPORTED for KV4_VALUES_BF16,
  * KV4_ERR_INVALID_ARG for the other handles), signs and value rotation included.
  *   out          device [B][Hq][D] of out_dtype, 16-byte aligned; lse fp32 [B][Hq] or NULL
  *   workspace    kv4_decode_shared_workspace_bytes(B, n_groups) bytes, as for kv4_decode_attn
