@@ -316,13 +316,13 @@ kv4_status kv4_bf16_decode_attn(kv4_cache* cache, int layer, int B, const void* 
  * sequences.  Rows [group_start[i], group_start[i + 1]) of the batch form group i (device int32
  * [n_groups + 1], non-decreasing, within [0, B]; rows before the first and after the last group
  * share nothing), and the first prefix_len[i] positions (device int32 [n_groups]) of its sequences
- * lie in pages with the same contents; they are read through the page-table row of the group's
- * first sequence, which therefore lists pages for the whole prefix even where that sequence is
- * shorter, whole 16 positions at a time (what is left of prefix_len past a multiple of 16 is read
- * as each sequence's own).  The page ids of the other rows may be the same (pages shared)
- * or not (copies); where a prompt ends inside a page that each sequence continues in a page of
- * its own without a copy of the prompt's end, prefix_len counts the whole pages only.  A prefix
- * may be longer than some of its sequences; each attends what it would in kv4_decode_attn: its
+ * have the same contents.  What is shared is the prefix's whole pages, prefix_len[i] / page_size of
+ * them: they are read through the page-table row of the group's first sequence, which therefore
+ * lists them even where that sequence is shorter.  The positions after them are read as each
+ * sequence's own, since a page in which a prompt ends goes on with one sequence's answer; so a
+ * prompt's length serves as it is.  The page ids of the other rows may be the same (pages shared)
+ * or not (copies).  A prefix may be longer than some of its sequences; each attends what it would
+ * in kv4_decode_attn: its
  * own INT8 sink and recent rows, and the INT4 positions before its recent window.  Attention of
  * the INT4 cache with INT4 values (KV4_ERR_UNSUPPORTED for KV4_VALUES_BF16,
  * KV4_ERR_INVALID_ARG for the other handles), signs and value rotation included.

@@ -44,14 +44,14 @@ __device__ __forceinline__ bool unlikely(bool x) { return __builtin_expect(x, 0)
 //
 // Groups of consecutive batch rows share the pages of their prefix.  A segment is (group, KV head,
 // block of kRB query rows); a query row is one query head of one sequence.  Its units are the
-// 128-position tiles from the tile of the first position past the sinks to the last whole 16
-// positions of the prefix.  The units of all segments form one sequence, thread block c takes
+// 128-position tiles from the tile of the first position past the sinks to the end of the prefix's last
+// whole page (what lies past it is in each sequence's own page).  The units of all segments form one sequence, thread block c takes
 // [c Q, (c + 1) Q) of it and writes one partial (o, m, l) per row of every segment it touches, at
 // index c + segment number.
 
 struct Group {
   int b0, n;    // rows of the batch
-  int te;       // prefix end, in 16-position tiles
+  int te;       // end of the prefix's whole pages, in 16-position tiles
   int tiles;    // units of a segment
   int nrb;      // row blocks
 };
@@ -63,7 +63,8 @@ __device__ __forceinline__ Group load_group(const DecodeArgs& a, int gr, bool* b
   *bad = b0 < 0 || b1 < b0 || b1 > a.B;
   r.b0 = b0;
   r.n = *bad ? 0 : b1 - b0;
-  r.te = clamp_len(a.prefix_len[gr], a.stride * a.P) >> 4;
+  const int tpp = a.P >> 4, tl = clamp_len(a.prefix_len[gr], a.stride * a.P) >> 4;
+  r.te = a.tp_shift >= 0 ? tl >> a.tp_shift << a.tp_shift : tl / tpp * tpp;
   const int t0 = a.s >> 4;
   r.tiles = (r.n > 0 && 16 * r.te > a.s) ? (r.te - t0 + kTile / 16 - 1) / (kTile / 16) : 0;
   if (r.tiles == 0) r.te = 0;

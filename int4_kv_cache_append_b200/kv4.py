@@ -612,7 +612,8 @@ class Cache(_RopeCacheMixin):
     def decode_shared(self, layer, q, page_table, lens, group_start, prefix_len, out=None, lse=None, max_len_hint=0,
                       workspace=None, stream=None):
         """Decode of a batch whose row groups [group_start[i], group_start[i + 1]) share their first
-        prefix_len[i] positions; out has q's type unless given."""
+        prefix_len[i] positions (their whole pages; the rest is read as each row's own); out has q's type
+        unless given."""
         B, n = lens.numel(), prefix_len.numel()
         shape = (B, self.geo.num_q_heads, self.geo.head_dim)
         if q.shape != shape or page_table.size(0) < B:

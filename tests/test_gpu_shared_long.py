@@ -145,3 +145,11 @@ def test_enormous_queries_pick_the_largest_logit(kv4, f):
                 others = np.delete(x, at)
                 assert x[at] > 2 * others.max() > 0  # far more than 2^-11 ahead
                 assert np.all(np.abs(out[b, j] - v[at]) <= 1.05 * 2.0 ** -10 * np.abs(v[at]) + 2e-4)
+
+
+@pytest.mark.parametrize("P,prefix", [(64, [2000, 130]), (48, [1000, 47]), (32, [527, 300])])
+def test_prefix_that_ends_inside_a_page(kv4, P, prefix):
+    """What lies past a prefix's last whole page is each row's own page, whatever prefix_len counts."""
+    r = L.to_gpu(L.batch(128, 4, 2, P, 4, 16, 128, [3, 2], prefix, [40, 1, 200, 30, 99], ends_differ=True))
+    out, lse = L.decode(r)
+    L.check(r, out, lse, L.picks_of(r, 4))
