@@ -292,7 +292,7 @@ def prepare(case, seed):
         s["k_read"], s["v_read"] = (torch.empty(N, case["Hkv"], case["D"], dtype=BF16, device="cuda") for _ in range(2))
         fill_slot, fill_pos, limit = _dev(p["old_slot"]), _dev(p["old_pos"]), _dev(p["old"])
     else:
-        s |= {"start": _dev(p["start"]), "prefix": _dev(p["prefix"] // case["P"] * case["P"]), "group": _dev(p["group"])}
+        s |= {"start": _dev(p["start"]), "prefix": _dev(p["prefix"]), "group": _dev(p["group"])}
         s["q"] = _randn(gen, slots, case["Hq"], case["D"])
         rows = np.zeros((case["groups"], max(p["per"])), np.int64)
         valid = np.zeros(rows.shape, bool)
