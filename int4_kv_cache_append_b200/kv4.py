@@ -10,6 +10,7 @@ fallback path, and importing this module fails loudly when the library is missin
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -184,6 +185,18 @@ def _stream(stream) -> int | None:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+_NO_STREAM = contextlib.nullcontext()
+
+
+def _on_stream(stream):
+    """Context in which torch allocates for work on the stream (the current one: None)."""
+    if stream is None:
+        return _NO_STREAM
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 _DTYPES = {torch.float32: KV4_F32, torch.bfloat16: KV4_BF16, torch.float16: KV4_F16}
@@ -520,6 +533,32 @@ class Rope:
         return q_out, k_out
 
 
+class _Workspaces:
+    """Device buffers of the calls that are given none: one for each stream, since calls on one stream do
+    not overlap, grown by half at least when a call needs more (so that a batch whose shape changes every
+    step settles on one).  During a capture a call gets a buffer from the graph's own memory instead: it
+    lives as long as the graph, whatever later calls need."""
+
+    def __init__(self):
+        self._bufs = {}
+
+    def get(self, nbytes: int, device, stream=None) -> torch.Tensor:
+        with _on_stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return torch.empty(nbytes, dtype=torch.uint8, device=device)
+            key = _stream(None)
+            buf = self._bufs.get(key)
+            if buf is None or buf.numel() < nbytes:
+                size = nbytes if buf is None else max(nbytes, buf.numel() * 3 // 2)
+                self._bufs.pop(key, None)
+                del buf
+                buf = self._bufs[key] = torch.empty(size, dtype=torch.uint8, device=device)
+            return buf
+
+    def clear(self) -> None:
+        self._bufs.clear()
+
+
 class _RopeCacheMixin:
     """kv4_append_rope and kv4_gather of a cache object (both kinds of handle)."""
 
@@ -564,8 +603,7 @@ class Cache(_RopeCacheMixin):
             self.pool.fill_(fill)
             self.side.fill_(fill)
         self.handle = kv4_cache_init(self.cfg, self.pool, self.side)
-        self._ws = None
-        self._shared_ws = {}
+        self._ws = _Workspaces()
 
     def layer_views(self, layer: int):
         """(pages of the layer, side cache of the layer) as uint8 views."""
@@ -584,30 +622,22 @@ class Cache(_RopeCacheMixin):
         kv4_append(self.handle, layer, int(seq_slot.numel()), K, dtype_code(K), V, dtype_code(V), seq_slot, pos,
                    lens_after, page_table, int(page_table.shape[1]), stream)
 
-    def workspace(self, B: int) -> torch.Tensor:
-        n = kv4_decode_workspace_bytes(self.handle, B)
-        if self._ws is None or self._ws.numel() < n:
-            self._ws = torch.empty(n, dtype=torch.uint8, device=self.pool.device)
-        return self._ws
+    def workspace(self, B: int, stream=None) -> torch.Tensor:
+        """The cache's workspace for calls on the stream; it may be larger than the call needs."""
+        return self._ws.get(kv4_decode_workspace_bytes(self.handle, B), self.pool.device, stream)
 
     def decode(self, layer, q, page_table, lens, out=None, lse=None, max_len_hint=0, workspace=None, stream=None):
         B = int(lens.numel())
         if out is None:
             out = torch.empty((B, self.geo.num_q_heads, self.geo.head_dim), dtype=torch.float32, device=q.device)
-        ws = workspace if workspace is not None else self.workspace(B)
+        ws = workspace if workspace is not None else self.workspace(B, stream)
         kv4_decode_attn(self.handle, layer, B, q, dtype_code(q), page_table, int(page_table.shape[1]), lens,
                         max_len_hint, out, lse, ws, ws.numel(), stream)
         return out
 
-    def shared_workspace(self, B: int, n_groups: int) -> torch.Tensor:
-        """The cache's workspace for this batch shape.  It is kept (a captured graph may hold it);
-        calls that overlap on the GPU need workspaces of their own."""
-        ws = self._shared_ws.get((B, n_groups))
-        if ws is None:
-            ws = torch.empty(kv4_decode_shared_workspace_bytes(self.handle, B, n_groups), dtype=torch.uint8,
-                             device=self.pool.device)
-            self._shared_ws[(B, n_groups)] = ws
-        return ws
+    def shared_workspace(self, B: int, n_groups: int, stream=None) -> torch.Tensor:
+        """The cache's workspace for calls on the stream; it may be larger than the call needs."""
+        return self._ws.get(kv4_decode_shared_workspace_bytes(self.handle, B, n_groups), self.pool.device, stream)
 
     def decode_shared(self, layer, q, page_table, lens, group_start, prefix_len, out=None, lse=None, max_len_hint=0,
                       workspace=None, stream=None):
@@ -627,7 +657,7 @@ class Cache(_RopeCacheMixin):
         if lse is not None and (lse.shape != shape[:2] or lse.dtype is not torch.float32):
             raise ValueError("lse float32 [B][Hq] expected")
         if workspace is None:
-            workspace = self.shared_workspace(B, n)
+            workspace = self.shared_workspace(B, n, stream)
         elif workspace.dtype is not torch.uint8:
             raise ValueError("workspace: uint8 tensor expected")
         kv4_decode_attn_shared(self.handle, layer, B, q, dtype_code(q), page_table, page_table.size(1), lens, n,
@@ -636,6 +666,7 @@ class Cache(_RopeCacheMixin):
         return out
 
     def close(self):
+        self._ws.clear()
         if self.handle:
             kv4_cache_destroy(self.handle)
             self.handle = None
@@ -655,28 +686,27 @@ class BF16Cache(_RopeCacheMixin):
         self.cfg = geo.c()
         self.pool = torch.empty(max(kv4_bf16_query_sizes(self.cfg), 16), dtype=torch.uint8, device=device)
         self.handle = kv4_bf16_cache_init(self.cfg, self.pool)
-        self._ws = None
+        self._ws = _Workspaces()
 
     def append(self, layer, K, V, seq_slot, pos, page_table, stream=None):
         kv4_bf16_append(self.handle, layer, int(seq_slot.numel()), K, dtype_code(K), V, dtype_code(V), seq_slot, pos,
                         page_table, int(page_table.shape[1]), stream)
 
-    def workspace(self, B: int) -> torch.Tensor:
-        n = kv4_bf16_decode_workspace_bytes(self.handle, B)
-        if self._ws is None or self._ws.numel() < n:
-            self._ws = torch.empty(n, dtype=torch.uint8, device=self.pool.device)
-        return self._ws
+    def workspace(self, B: int, stream=None) -> torch.Tensor:
+        """The cache's workspace for calls on the stream; it may be larger than the call needs."""
+        return self._ws.get(kv4_bf16_decode_workspace_bytes(self.handle, B), self.pool.device, stream)
 
     def decode(self, layer, q, page_table, lens, out=None, lse=None, max_len_hint=0, workspace=None, stream=None):
         B = int(lens.numel())
         if out is None:
             out = torch.empty((B, self.geo.num_q_heads, self.geo.head_dim), dtype=torch.float32, device=q.device)
-        ws = workspace if workspace is not None else self.workspace(B)
+        ws = workspace if workspace is not None else self.workspace(B, stream)
         kv4_bf16_decode_attn(self.handle, layer, B, q, dtype_code(q), page_table, int(page_table.shape[1]), lens,
                              max_len_hint, out, lse, ws, ws.numel(), stream)
         return out
 
     def close(self):
+        self._ws.clear()
         if self.handle:
             kv4_cache_destroy(self.handle)
             self.handle = None
