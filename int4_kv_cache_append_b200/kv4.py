@@ -199,6 +199,18 @@ def _on_stream(stream):
     return torch.cuda.stream(stream)
 
 
+def _new(shape, dtype, device, stream):
+    """Tensor that a call on the stream writes.  It belongs to that stream, so that its memory has no work of
+    another one pending; the current stream may read it too (once it has waited for the call) before it
+    is used again."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on_stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 _DTYPES = {torch.float32: KV4_F32, torch.bfloat16: KV4_BF16, torch.float16: KV4_F16}
 
 
@@ -502,7 +514,7 @@ class Rope:
             raise ValueError("norm weights: one type and size expected")
         self.geo, self.q_weight, self.k_weight, self.eps = geo, q_weight, k_weight, eps
         self.cfg = geo.c()
-        self.table = torch.empty((max(geo.max_pos, 0), max(geo.rotary_dim, 0) // 2, 2), dtype=torch.float32, device=device)
+        self.table = _new((max(geo.max_pos, 0), max(geo.rotary_dim, 0) // 2, 2), torch.float32, device, stream)
         self.build(stream)
         w = q_weight if q_weight is not None else k_weight
         self.params = kv4_rope_params(self.table.data_ptr(), geo.max_pos, geo.rotary_dim, geo.layout,
@@ -526,9 +538,9 @@ class Rope:
         if x is not None:
             self.check_head_dim(x.shape[-1])
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = _new(q.shape, q.dtype, q.device, stream)
         if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            k_out = _new(k.shape, k.dtype, k.device, stream)
         kv4_rope(self.params, q, k, pos, q_out, k_out, stream)
         return q_out, k_out
 
@@ -570,7 +582,7 @@ class _RopeCacheMixin:
         if K.shape[1:] != (g.num_kv_heads, g.head_dim) or (q is not None and q.shape[1:] != (g.num_q_heads, g.head_dim)):
             raise ValueError("q [T][Hq][D] and K, V [T][Hkv][D] of the cache's geometry expected")
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = _new(q.shape, q.dtype, q.device, stream)
         kv4_append_rope(self.handle, layer, rope.params, q, K, V, seq_slot, pos, lens_after, page_table,
                         page_table.size(1), q_out, stream)
         return q_out
@@ -581,8 +593,8 @@ class _RopeCacheMixin:
         if pos.numel() != T:
             raise ValueError("one position per seq_slot expected")
         shape = (T, self.geo.num_kv_heads, self.geo.head_dim)
-        k_out = torch.empty(shape, dtype=dtype, device=pos.device) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=dtype, device=pos.device) if v_out is None else v_out
+        k_out = _new(shape, dtype, pos.device, stream) if k_out is None else k_out
+        v_out = _new(shape, dtype, pos.device, stream) if v_out is None else v_out
         if k_out.shape != shape or v_out.shape != shape or k_out.dtype != v_out.dtype:
             raise ValueError("k_out and v_out [T][Hkv][D] of one type expected")
         kv4_gather(self.handle, layer, T, seq_slot, pos, lens, page_table, page_table.size(1), k_out, v_out,
@@ -629,7 +641,7 @@ class Cache(_RopeCacheMixin):
     def decode(self, layer, q, page_table, lens, out=None, lse=None, max_len_hint=0, workspace=None, stream=None):
         B = int(lens.numel())
         if out is None:
-            out = torch.empty((B, self.geo.num_q_heads, self.geo.head_dim), dtype=torch.float32, device=q.device)
+            out = _new((B, self.geo.num_q_heads, self.geo.head_dim), torch.float32, q.device, stream)
         ws = workspace if workspace is not None else self.workspace(B, stream)
         kv4_decode_attn(self.handle, layer, B, q, dtype_code(q), page_table, int(page_table.shape[1]), lens,
                         max_len_hint, out, lse, ws, ws.numel(), stream)
@@ -651,7 +663,7 @@ class Cache(_RopeCacheMixin):
         if group_start.numel() != n + 1:
             raise ValueError("group_start: one entry more than prefix_len expected")
         if out is None:
-            out = torch.empty(shape, dtype=q.dtype, device=q.device)
+            out = _new(shape, q.dtype, q.device, stream)
         elif out.shape != shape:
             raise ValueError("out [B][Hq][D] expected")
         if lse is not None and (lse.shape != shape[:2] or lse.dtype is not torch.float32):
@@ -699,7 +711,7 @@ class BF16Cache(_RopeCacheMixin):
     def decode(self, layer, q, page_table, lens, out=None, lse=None, max_len_hint=0, workspace=None, stream=None):
         B = int(lens.numel())
         if out is None:
-            out = torch.empty((B, self.geo.num_q_heads, self.geo.head_dim), dtype=torch.float32, device=q.device)
+            out = _new((B, self.geo.num_q_heads, self.geo.head_dim), torch.float32, q.device, stream)
         ws = workspace if workspace is not None else self.workspace(B, stream)
         kv4_bf16_decode_attn(self.handle, layer, B, q, dtype_code(q), page_table, int(page_table.shape[1]), lens,
                              max_len_hint, out, lse, ws, ws.numel(), stream)

@@ -93,3 +93,67 @@ def test_calls_on_two_streams_have_their_own_workspaces(kv4):
             cache.decode_shared(0, q, table, lens, *gs, out=o[1], stream=st.cuda_stream)
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for o in outs for x, y in zip(o, want))
+
+
+def calls(kv4):
+    """name -> call(stream) that makes its own output."""
+    cache, table, lens, q = small(kv4, L=200)
+    bf = small(kv4, L=200, cls="BF16Cache")
+    rope = kv4.Rope(kv4.RopeGeometry(64, 256))
+    T = 64
+    x = torch.randn(T, 8, 64, device="cuda", dtype=torch.bfloat16)
+    pos, slot = i32(np.arange(T) + 100), i32(np.arange(T))
+    gs = groups(64, 4)
+    return {
+        "table": lambda st: kv4.Rope(kv4.RopeGeometry(64, 256), stream=st).table,
+        "rope-q": lambda st: rope.apply(x[:, :4], None, pos, stream=st)[0],
+        "rope-k": lambda st: rope.apply(None, x[:, 4:6], pos, stream=st)[1],
+        "append": lambda st: cache.append_rope(0, rope, x[:, :4], x[:, 4:6], x[:, 6:], slot, pos, lens, table, stream=st),
+        "gather-k": lambda st: cache.gather(0, slot, pos, table, lens, stream=st)[0],
+        "gather-v": lambda st: cache.gather(0, slot, pos, table, lens, stream=st)[1],
+        "decode": lambda st: cache.decode(0, q, table, lens, stream=st),
+        "shared": lambda st: cache.decode_shared(0, q, table, lens, *gs, stream=st),
+        "bf16": lambda st: bf[0].decode(0, bf[3], *bf[1:3], stream=st),
+    }
+
+
+NAMES = ("table", "rope-q", "rope-k", "append", "gather-k", "gather-v", "decode", "shared", "bf16")
+DELAY = 100_000_000  # cycles
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+@pytest.mark.parametrize("name", NAMES)
+def test_output_on_another_stream_is_not_pending_memory(kv4, name, raw):
+    """Memory that the current stream still has writes pending for is not handed to a call on another."""
+    call = calls(kv4)[name]
+    st = torch.cuda.Stream()
+    want = call(None).clone()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = [torch.empty_like(want) for _ in range(64)]
+    torch.cuda._sleep(DELAY)
+    for x in held:
+        x.fill_(7)
+    del held, x
+    got = call(st.cuda_stream if raw else st)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_output_on_another_stream_lives_until_the_current_one_has_read_it(kv4, name):
+    call = calls(kv4)[name]
+    st = torch.cuda.Stream()
+    want = call(None).clone()
+    kept = torch.empty_like(want)
+    torch.cuda.synchronize()
+    got = call(st)
+    torch.cuda.current_stream().wait_stream(st)
+    torch.cuda._sleep(DELAY)
+    kept.copy_(got)
+    del got
+    with torch.cuda.stream(st):  # what st allocates next
+        for _ in range(64):
+            torch.empty_like(want).fill_(7)
+    torch.cuda.synchronize()
+    assert torch.equal(kept, want)
