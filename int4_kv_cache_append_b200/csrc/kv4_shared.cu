@@ -199,6 +199,7 @@ struct SmemPrefix {
   uint64_t raw_full[kRaw], raw_empty[kRaw];
   uint64_t k_ready[2], v_ready[2], qk_done[2], p_ready[2], pv_done[2];
   uint64_t q_ready;
+  uint64_t drained;           // the MMA warp's last commit
   uint64_t stall;             // never arrived on (kv4_debug_force_wait_timeout)
   uint32_t tmem;
   int abort;
@@ -217,31 +218,36 @@ struct Cols {
 template <typename T>
 __device__ __forceinline__ T uniform(T x) { return __shfl_sync(FULL, x, 0); }
 
-// Up to 64 polls of a phase.
+// Up to N polls of a phase.
+template <int N>
 __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
       "KV4_POLL_%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra KV4_DONE_%=;\n"
-      " add.u32 n, n, 1;\n setp.lt.u32 q, n, 64;\n @q bra KV4_POLL_%=;\n"
+      " add.u32 n, n, 1;\n setp.lt.u32 q, n, %3;\n @q bra KV4_POLL_%=;\n"
       "KV4_DONE_%=:\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "n"(N)
       : "memory");
   return ok != 0;
 }
 
-// A bounded wait that gives up when any warp of the block has: every role then runs its loop to the
-// end without waiting, so that all of them reach the end of the kernel.  A warpgroup waits by one
-// warp, the others at a hardware barrier: polls by every warp were half of the issued instructions.
+// A bounded wait that gives up when any warp of the block has.  Then the warps that meet at hardware
+// barriers run their loops to the end, each wait costing a few polls, on whatever the buffers hold; the
+// copy warp starts no more copies, and the last commit's barrier says when the products are done.  A
+// warpgroup waits by one warp, the others at a hardware barrier: polls by every warp were half of the
+// issued instructions.
 __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err, uint64_t limit_ns) {
   const uint32_t at = smem_u32(bar);
-  if (unlikely(!poll(at, parity))) {
-    const uint64_t t0 = global_timer_ns();
+  if (unlikely(!poll<4>(at, parity))) {
+    uint64_t t0 = 0;
 #pragma unroll 1
-    for (uint32_t it = 1; !poll(at, parity); ++it) {
-      if (*abort) return;
-      if (global_timer_ns() - t0 > limit_ns || it >= kWaitLimitPolls / 64) {
+    for (uint32_t it = 0;; ++it) {
+      if (*abort || poll<64>(at, parity)) return;
+      const uint64_t t = global_timer_ns();
+      if (it == 0) t0 = t;
+      if (t - t0 > limit_ns || it >= kWaitLimitPolls / 64) {
         *abort = 1;
         atomicOr(err, KV4_DEVERR_WAIT_LIMIT);
         return;
@@ -559,6 +565,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
       mbar_init(&sm.pv_done[i], 1);
     }
     mbar_init(&sm.q_ready, kSoftWarps);
+    mbar_init(&sm.drained, 1);
     mbar_init(&sm.stall, 1);
     fence_mbar_init();
     sm.abort = 0;
@@ -832,7 +839,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
     }
   } else if (warp == kCopyWarp) {
     // ------------------------------------------------------------------ copies
-    while (walk_next<G>(a, sm.plan, s, lane)) {
+    // After an abort none is started: a buffer's barrier may still wait for the bytes of its last ones, and
+    // "empty" no longer means that it has been read.  i counts the units whose copies were started.
+    bool stop = false;
+    while (!stop && walk_next<G>(a, sm.plan, s, lane)) {
       const int te = s.te;
       const int32_t* row = a.page_table + static_cast<size_t>(s.b0) * a.stride;
       const uint8_t* head = a.pool + static_cast<size_t>(s.g) * (a.P / 16) * Gm::T4B;
@@ -848,8 +858,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
         const int st = static_cast<int>(i % kRaw);
         const int next = i + 1 != i1 ? page_of(ti + 8) : 0;
         if (i >= kRaw) wait(&sm.raw_empty[st], i / kRaw - 1);
-        const bool in = lane < 8 && ti < te, good = in && page >= 0 && page < a.max_pages && !*abort;
-        if (in && !good && !*abort) atomicOr(a.err, KV4_DEVERR_PAGE_RANGE);
+        stop = __any_sync(FULL, *abort);
+        if (stop) break;
+        const bool in = lane < 8 && ti < te, good = in && page >= 0 && page < a.max_pages;
+        if (in && !good) atomicOr(a.err, KV4_DEVERR_PAGE_RANGE);
         const uint32_t ok = __ballot_sync(FULL, good);
         if (lane == 0) {
           sm.ok[st] = ok;
@@ -906,12 +918,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
       }
       i = i1;
     }
-    // the last products are done before TMEM is freed, however the loop ended
-    if (lane == 0)
-      for (u32 k = i > 2 ? i - 2 : 0; k < i; ++k) {
-        mbar_wait_bounded(&sm.qk_done[k & 1], (k >> 1) & 1u, a.err, kWaitLimitNs);
-        mbar_wait_bounded(&sm.pv_done[k & 1], (k >> 1) & 1u, a.err, kWaitLimitNs);
-      }
+    // all products are done before TMEM is freed, however the loop ended (after an abort, waits that are not
+    // awaited leave the parities of qk_done and pv_done meaningless)
+    if (i) {
+      tc::commit(&sm.drained, leader);
+      if (leader) mbar_wait_bounded(&sm.drained, 0u, a.err, kWaitLimitNs);
+    }
     __syncwarp();
   }
   tc::fence_before();

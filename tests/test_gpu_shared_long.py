@@ -153,3 +153,25 @@ def test_prefix_that_ends_inside_a_page(kv4, P, prefix):
     r = L.to_gpu(L.batch(128, 4, 2, P, 4, 16, 128, [3, 2], prefix, [40, 1, 200, 30, 99], ends_differ=True))
     out, lse = L.decode(r)
     L.check(r, out, lse, L.picks_of(r, 4))
+
+
+@pytest.mark.parametrize("name", ["ten-units-a-block", "two-row-blocks-d64-p48"])
+def test_waits_that_run_out_in_mid_pipeline(kv4, name):
+    """The bounded waits made to run out (1 ms) with most units of every block to come: the error bit is set,
+    the call ends soon after, and the next one is right."""
+    r = L.to_gpu(L.batch(**CASES[name]))
+    want = L.decode(r)
+    ws = torch.full((kv4.kv4_decode_shared_workspace_bytes(r.cache.handle, r.B, len(r.sizes)),), 0xA5, dtype=torch.uint8, device="cuda")
+    at = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    kv4.kv4_debug_force_wait_timeout(r.cache.handle, True)
+    try:
+        at[0].record()
+        L.decode(r, workspace=ws)
+        at[1].record()
+        torch.cuda.synchronize()
+    finally:
+        kv4.kv4_debug_force_wait_timeout(r.cache.handle, False)
+    assert kv4.kv4_get_device_error() & kv4.KV4_DEVERR_WAIT_LIMIT
+    assert at[0].elapsed_time(at[1]) < 200
+    got = L.decode(r, workspace=ws)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
