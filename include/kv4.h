@@ -329,7 +329,8 @@ kv4_status kv4_bf16_decode_attn(kv4_cache* cache, int layer, int B, const void* 
  *   out          device [B][Hq][D] of out_dtype, 16-byte aligned; lse fp32 [B][Hq] or NULL
  *   workspace    kv4_decode_shared_workspace_bytes(B, n_groups) bytes, as for kv4_decode_attn
  * Precision: within the prefix the rotated query and the probabilities enter the products as fp16
- * (11 bits), keys as exact codes and values as fp16; statistics and sums are fp32.  The other
+ * (11 bits; a probability below 2^-29 of the largest that its thread block has seen is taken as
+ * zero), keys as exact codes and values as fp16; statistics and sums are fp32.  The other
  * arguments are those of kv4_decode_attn.  Three launches: prefix, own positions, merge.
  */
 kv4_status kv4_decode_shared_workspace_bytes(const kv4_cache* cache, int B, int n_groups, size_t* bytes);

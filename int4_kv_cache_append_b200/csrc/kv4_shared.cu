@@ -15,8 +15,8 @@
 // A thread block is 26 warps: four softmax warpgroups (16 of the 64 columns each, a thread per
 // position), a warpgroup unpacking keys, one unpacking values, a warp of bulk copies and a warp
 // that issues the MMAs; K, V, S and P have two buffers, the packed tiles four.  The running maximum
-// of a row is raised only when a logit exceeds it by more than 11 (P then stays below 2^11, and 16
-// times that inside fp16): the first unit of a segment sets it, later ones seldom rescale O.
+// of a row is set 4 (log2) below its largest logit and raised only when one exceeds it by more than
+// 15 (P then stays inside fp16): the first unit of a segment sets it, later ones seldom rescale O.
 //
 // What bounds it: 16 prompts of up to 8 K positions with up to 16 answers each, 32 + 8 heads of 128,
 // take 147 us (one by one the prefix kernel 107, own positions 37, merge 10) for 217 MB that have to be
@@ -166,7 +166,15 @@ constexpr int kSoftWarps = 4 * kSoftGroups, kKeyWarp0 = kSoftWarps, kValWarp0 = 
               kMmaWarp = kCopyWarp + 1, kSoftThreads = 32 * kSoftWarps;
 constexpr int kPrefixThreads = 32 * (kMmaWarp + 1);
 constexpr float kUnset = -1e30f;   // running maximum of a row that has seen no position
-constexpr float kGrow = 11.f;      // a logit this far (log2) above the running maximum raises it
+// A raised running maximum is set kLift (log2) below the largest logit, so probabilities start at 2^kLift and
+// what fp16 takes as zero is below 2^(-25 - kLift) of the largest: the 10^5 positions that a thread block
+// may take lose 2^-12 of it at most, less than the roundings (from 1 on they lost 2^-8, which the sums
+// counted and the products did not).  A logit kGrow above raises it again: probabilities end at 2^15.
+// With 4 a logit may grow by 2^11 before that, as it could with 0 (no difference in time); with 6 and 8
+// the rescaling cost 1% and 2 to 4% (128 answers to one prompt of 16 K: 158.8, 160.6, 164.9 us).
+constexpr float kLift = 4.f;
+constexpr float kGrow = 15.f;
+constexpr float kGrowLarge = 11.f;  // with values taken times 1/16: probabilities are then times 16
 constexpr float kQShift = 64.f;    // queries enter fp16 times this: typical ones are then near one
 
 // The units of this thread block, segment by segment: every warp walks them on its own.  The state
@@ -471,7 +479,7 @@ __device__ __noinline__ void soft_unit_slow(SmemPrefix<D>& sm, const SoftUnit u,
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = fmaxf(top, logit(c0 + j, r[j]) + neg_max(c0 + j));
     }
-    raise = group_or(id, top > kGrow);
+    raise = group_or(id, top > (large ? kGrowLarge : kGrow));
   }
   if (raise) {
     // column maxima over the 128 positions
@@ -496,7 +504,7 @@ __device__ __noinline__ void soft_unit_slow(SmemPrefix<D>& sm, const SoftUnit u,
     if (u.w4 == 0 && u.lane < 8 * u.nch) {
       const int n = 8 * (u.wg + kSoftGroups * (u.lane >> 3)) + (u.lane & 7);
       const float m0 = -neg_max(n);
-      const float m1 = fmaxf(fmaxf(sm.red[u.wg][0][u.lane], sm.red[u.wg][1][u.lane]), fmaxf(sm.red[u.wg][2][u.lane], sm.red[u.wg][3][u.lane]));
+      const float m1 = fmaxf(fmaxf(sm.red[u.wg][0][u.lane], sm.red[u.wg][1][u.lane]), fmaxf(sm.red[u.wg][2][u.lane], sm.red[u.wg][3][u.lane])) - kLift;
       const bool up = m1 > m0;
       sm.alpha[n] = !up ? 1.f : m0 == kUnset ? 0.f : exp2_fast(m0 - m1);
       if (up) neg_max(n) = -m1;

@@ -175,3 +175,23 @@ def test_waits_that_run_out_in_mid_pipeline(kv4, name):
     assert at[0].elapsed_time(at[1]) < 200
     got = L.decode(r, workspace=ws)
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("below", [25.6, 27.0])
+def test_many_small_probabilities_are_not_lost(kv4, below):
+    """One position ahead of all others by 2^`below`: the 1200 after it that a thread block takes with it add
+    up to 2e-5 of the sum, and with values of 1000 where all other values are zero they are the output."""
+    def edit(g, K, V):
+        u = np.full(K.shape[2], 1 / np.sqrt(K.shape[2]), np.float32)
+        K *= 0.05
+        K -= (K @ u)[..., None] * u
+        K[40] += (below * np.log(2) * np.sqrt(K.shape[2]) / 20) * u
+        V *= 100
+        V += 1000
+        V[:41] = 0
+        V[1280:] = 0
+    r = L.to_gpu(L.batch(128, 4, 8, 16, 0, 0, 128, [2, 2], [12000, 12000], [0, 16, 0, 0], edit=edit))
+    assert L.units(r) > 10 * sms()
+    q = np.full_like(r.q, 20 / np.sqrt(r.D))
+    out, lse = L.decode(r, q)
+    L.check(r, out, lse, [(b, j) for b in range(2) for j in range(4)], q=q, floor=2.0 ** -29)
