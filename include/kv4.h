@@ -314,8 +314,8 @@ kv4_status kv4_bf16_decode_attn(kv4_cache* cache, int layer, int B, const void* 
  * kv4_decode_attn_shared: kv4_decode_attn for a batch whose sequences share long prefixes, as the
  * answers sampled for one prompt do: each group's prefix is read and decoded once for all of its
  * sequences.  Rows [group_start[i], group_start[i + 1]) of the batch form group i (device int32
- * [n_groups + 1], non-decreasing, within [0, B]; rows before the first and after the last group
- * share nothing), and the first prefix_len[i] positions (device int32 [n_groups]) of its sequences
+ * [n_groups + 1], non-decreasing, within [0, B]; rows before the first and after the last group, and
+ * a group of one row, share nothing), and the first prefix_len[i] positions (device int32 [n_groups]) of its sequences
  * have the same contents.  What is shared is the prefix's whole pages, prefix_len[i] / page_size of
  * them: they are read through the page-table row of the group's first sequence, which therefore
  * lists them even where that sequence is shorter.  The positions after them are read as each

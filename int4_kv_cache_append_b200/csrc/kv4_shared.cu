@@ -42,7 +42,8 @@ __device__ __forceinline__ bool unlikely(bool x) { return __builtin_expect(x, 0)
 
 // ------------------------------------------------------------------ the prefix schedule
 //
-// Groups of consecutive batch rows share the pages of their prefix.  A segment is (group, KV head,
+// Groups of consecutive batch rows share the pages of their prefix; a single row shares nothing and is left
+// to the split-K kernel (64 of them over 4 K positions each: 207 us here, 70 there).  A segment is (group, KV head,
 // block of kRB query rows); a query row is one query head of one sequence.  Its units are the
 // 128-position tiles from the tile of the first position past the sinks to the end of the prefix's last
 // whole page (what lies past it is in each sequence's own page).  The units of all segments form one sequence, thread block c takes
@@ -66,7 +67,7 @@ __device__ __forceinline__ Group load_group(const DecodeArgs& a, int gr, bool* b
   const int tpp = a.P >> 4, tl = clamp_len(a.prefix_len[gr], a.stride * a.P) >> 4;
   r.te = a.tp_shift >= 0 ? tl >> a.tp_shift << a.tp_shift : tl / tpp * tpp;
   const int t0 = a.s >> 4;
-  r.tiles = (r.n > 0 && 16 * r.te > a.s) ? (r.te - t0 + kTile / 16 - 1) / (kTile / 16) : 0;
+  r.tiles = (r.n > 1 && 16 * r.te > a.s) ? (r.te - t0 + kTile / 16 - 1) / (kTile / 16) : 0;
   if (r.tiles == 0) r.te = 0;
   r.nrb = (r.n * G + kRB - 1) / kRB;
   return r;

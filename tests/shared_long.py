@@ -19,10 +19,12 @@ class Batch:
 
 
 def units(r):
-    """Units of the prefix kernel: per group, KV head and block of query rows, the 128-position tiles
+    """Units of the prefix kernel: per group of two rows and more, KV head and block of query rows, the 128-position tiles
     from the tile of the first position past the sinks to the end of the whole pages of the prefix."""
     total = 0
     for n, p in zip(r.sizes, r.prefix):
+        if n == 1:
+            continue
         te = p // r.P * r.P // 16
         tiles = -(-(te - r.s // 16) // (UNIT // 16)) if 16 * te > r.s else 0
         total += r.Hkv * -(-n * r.G // ROWS) * tiles

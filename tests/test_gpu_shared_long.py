@@ -28,7 +28,7 @@ def sms():
 
 # (name, arguments of batch)
 CASES = {
-    "ten-units-a-block": dict(D=128, G=4, Hkv=8, P=16, s=4, w=16, h=128, sizes=[2, 1, 3], prefix=[9000, 5003, 9007], past=[40, 1, 300, 5, 77, -700]),
+    "ten-units-a-block": dict(D=128, G=4, Hkv=8, P=16, s=4, w=16, h=128, sizes=[2, 1, 3, 2], prefix=[9000, 5003, 9007, 3000], past=[40, 1, 300, 5, 77, -700, 8, 9]),
     "two-row-blocks": dict(D=128, G=4, Hkv=4, P=64, s=16, w=32, h=64, sizes=[17, 4], prefix=[8000, 6050], past=[3 * i + 1 for i in range(21)]),
     "two-row-blocks-d64-p48": dict(D=64, G=2, Hkv=4, P=48, s=0, w=24, h=16, sizes=[40, 2], prefix=[6000, 9001], past=[2 * i for i in range(42)]),
     "one-query-head-d64": dict(D=64, G=1, Hkv=8, P=32, s=4, w=0, h=64, sizes=[3, 2, 2], prefix=[4111, 6000, 3001], past=[0, 9, 2, 30, 4, 50, 6]),
@@ -195,3 +195,15 @@ def test_many_small_probabilities_are_not_lost(kv4, below):
     q = np.full_like(r.q, 20 / np.sqrt(r.D))
     out, lse = L.decode(r, q)
     L.check(r, out, lse, [(b, j) for b in range(2) for j in range(4)], q=q, floor=2.0 ** -29)
+
+
+def test_a_group_of_one_row_shares_nothing(kv4):
+    """Rows that form groups of one get what a call without groups gives, bit for bit."""
+    r = L.to_gpu(L.batch(128, 4, 2, 16, 4, 16, 128, [1, 3, 1, 1, 2], [900, 700, 30, 2000, 500], [5, 6, 7, 8, 9, 10, 11, 12]))
+    out, lse = L.decode(r)
+    L.check(r, out, lse, L.picks_of(r, 4))
+    r.start_d, r.prefix_d = r.start_d[:1], r.prefix_d[:0]
+    plain = L.decode(r)
+    r.start_d, r.prefix_d = torch.arange(r.B + 1, device="cuda", dtype=torch.int32), torch.full((r.B,), 10000, device="cuda", dtype=torch.int32)
+    single = L.decode(r)
+    assert torch.equal(single[0], plain[0]) and torch.equal(single[1], plain[1])
