@@ -552,20 +552,27 @@ class _Workspaces:
     lives as long as the graph, whatever later calls need."""
 
     def __init__(self):
-        self._bufs = {}
+        self._bufs = {}  # stream -> (what the last call asked for, its buffer)
 
-    def get(self, nbytes: int, device, stream=None) -> torch.Tensor:
-        with _on_stream(stream):
-            if torch.cuda.is_current_stream_capturing():
-                return torch.empty(nbytes, dtype=torch.uint8, device=device)
-            key = _stream(None)
-            buf = self._bufs.get(key)
-            if buf is None or buf.numel() < nbytes:
-                size = nbytes if buf is None else max(nbytes, buf.numel() * 3 // 2)
-                self._bufs.pop(key, None)
-                del buf
-                buf = self._bufs[key] = torch.empty(size, dtype=torch.uint8, device=device)
+    def get(self, size, args, device, stream=None) -> torch.Tensor:
+        """A buffer of at least size(*args) bytes for work on the stream."""
+        if stream is not None:
+            with _on_stream(stream):
+                return self.get(size, args, device)
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(size(*args), dtype=torch.uint8, device=device)
+        key = _stream(None)
+        last, buf = self._bufs.get(key, (None, None))
+        if last == (size, args):
             return buf
+        n = size(*args)
+        if buf is None or buf.numel() < n:
+            n = n if buf is None else max(n, buf.numel() * 3 // 2)
+            self._bufs.pop(key, None)
+            del buf
+            buf = torch.empty(n, dtype=torch.uint8, device=device)
+        self._bufs[key] = (size, args), buf
+        return buf
 
     def clear(self) -> None:
         self._bufs.clear()
@@ -636,7 +643,7 @@ class Cache(_RopeCacheMixin):
 
     def workspace(self, B: int, stream=None) -> torch.Tensor:
         """The cache's workspace for calls on the stream; it may be larger than the call needs."""
-        return self._ws.get(kv4_decode_workspace_bytes(self.handle, B), self.pool.device, stream)
+        return self._ws.get(kv4_decode_workspace_bytes, (self.handle, B), self.pool.device, stream)
 
     def decode(self, layer, q, page_table, lens, out=None, lse=None, max_len_hint=0, workspace=None, stream=None):
         B = int(lens.numel())
@@ -649,7 +656,7 @@ class Cache(_RopeCacheMixin):
 
     def shared_workspace(self, B: int, n_groups: int, stream=None) -> torch.Tensor:
         """The cache's workspace for calls on the stream; it may be larger than the call needs."""
-        return self._ws.get(kv4_decode_shared_workspace_bytes(self.handle, B, n_groups), self.pool.device, stream)
+        return self._ws.get(kv4_decode_shared_workspace_bytes, (self.handle, B, n_groups), self.pool.device, stream)
 
     def decode_shared(self, layer, q, page_table, lens, group_start, prefix_len, out=None, lse=None, max_len_hint=0,
                       workspace=None, stream=None):
@@ -706,7 +713,7 @@ class BF16Cache(_RopeCacheMixin):
 
     def workspace(self, B: int, stream=None) -> torch.Tensor:
         """The cache's workspace for calls on the stream; it may be larger than the call needs."""
-        return self._ws.get(kv4_bf16_decode_workspace_bytes(self.handle, B), self.pool.device, stream)
+        return self._ws.get(kv4_bf16_decode_workspace_bytes, (self.handle, B), self.pool.device, stream)
 
     def decode(self, layer, q, page_table, lens, out=None, lse=None, max_len_hint=0, workspace=None, stream=None):
         B = int(lens.numel())
