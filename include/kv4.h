@@ -349,10 +349,12 @@ kv4_status kv4_decode_attn_shared(kv4_cache* cache, int layer, int B, const void
  * base^(-2i/R), scaled for contexts beyond the trained length by
  *   KV4_ROPE_SCALE_LINEAR  f_i / factor (positions interpolated);
  *   KV4_ROPE_SCALE_NTK     base^(-2i/R) with base * factor^(R / (R - 2));
- *   KV4_ROPE_SCALE_YARN    ("YaRN: Efficient Context Window Extension of Large Language Models",
- *                          section 3.2): pairs that turn at least beta_fast times over
- *                          original_max_pos keep f_i, at most beta_slow times take f_i / factor, a
- *                          linear ramp over the pair index between; cos and sin are multiplied by
+ *   KV4_ROPE_SCALE_YARN    pairs that turn at least beta_fast times over original_max_pos keep f_i,
+ *                          at most beta_slow times take f_i / factor, a ramp between that is linear in
+ *                          the pair index, from the floor of the one border's index to the ceiling of
+ *                          the other's (as models are trained with it; section 3.2 of "YaRN: Efficient
+ *                          Context Window Extension of Large Language Models" has a ramp that is
+ *                          linear in the number of turns); cos and sin are multiplied by
  *                          attention_factor (0: 0.1 ln(factor) + 1 when factor > 1);
  *   KV4_ROPE_SCALE_BANDS   pairs that turn at least high_freq_factor times over original_max_pos
  *                          keep f_i, at most low_freq_factor times take f_i / factor, a blend that is
@@ -380,9 +382,10 @@ typedef struct {
 } kv4_rope_config;
 
 /*
- * kv4_rope_table: write the table the calls below read, fp32 [max_pos][R/2][2] (cos, sin), each entry
- * the fp64 value (of the angle p f_i taken in fp64) rounded once.  table: device, 16-byte aligned,
- * max_pos * R * 4 bytes.  A program builds it once; a caller's own table of that form serves as well.
+ * kv4_rope_table: write the table the calls below read, fp32 [max_pos][R/2][2] (cos, sin), computed in
+ * fp64 and rounded once: an entry is within half an fp32 step, plus (2^-50 p f_i + 2^-45) times the
+ * factor on cos and sin, of the exact value.  table: device, 16-byte aligned, max_pos * R * 4 bytes.  A
+ * program builds it once; a caller's own table of that form serves as well.
  */
 kv4_status kv4_rope_table(const kv4_rope_config* cfg, float* table, void* stream);
 

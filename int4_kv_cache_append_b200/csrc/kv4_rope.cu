@@ -87,8 +87,9 @@ __device__ __forceinline__ void store8(void* base, int dtype, long long i, const
 // ------------------------------------------------------------------ the table
 
 // Thread (pair i, run of kRun positions): the run's first angle by one fp64 sincospi of the turns
-// p f / 2 pi reduced exactly, then one fp64 complex product per position (relative error at most
-// kRun 2^-52, far below the fp32 rounding of the entries).  Four fp64 multiply-adds an entry instead
+// p f / 2 pi reduced exactly, then one fp64 complex product per position.  Absolute errors before the
+// rounding to fp32: 2^-50 p f by the turns (at most 7 fp64 roundings), 2^-45 by the products (each below
+// 7 2^-53).  Four fp64 multiply-adds an entry instead
 // of a sine and a cosine keep the kernel on the memory's side: it writes 8 bytes an entry.
 constexpr int kRun = 32;
 
@@ -300,10 +301,12 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& a, const Rotation<D>&
 
 // ------------------------------------------------------------------ kv4_rope
 
-// Warp (token, run of hpw heads): queries first, then keys.  Four blocks an SM (64 registers, a few
-// spilled) hide more of the loads' latency than three (80): 97 -> 92 us for 16383 tokens of 32 + 8
-// heads in bf16, 3.7 TB/s of the 6.55 a copy reaches.  What is left is latency and issue (2.7
-// instructions a cycle an SM): a norm's tree, its root and its products depend on one another.
+// Warp (token, run of hpw heads): queries first, then keys.  Four blocks an SM (64 registers, 128
+// bytes a thread spilled) hide more of the loads' latency than three (80): 97 -> 92 us for 16383 tokens of 32 + 8
+// heads in bf16, 3.7 TB/s of the 6.55 a copy reaches.  What is left is issue (66 M warp
+// instructions, 2.7 a cycle an SM, are 59 us at four a cycle, above the 52 of the bytes) and latency: types,
+// layout and norm are branches at run time around arrays held in registers, and a norm's tree, its root
+// and its products depend on one another.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 4) rope_kernel(RopeArgs a, int hpw) {
   pdl_launch_dependents();
