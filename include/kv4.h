@@ -332,6 +332,9 @@ kv4_status kv4_bf16_decode_attn(kv4_cache* cache, int layer, int B, const void* 
  * (11 bits; a probability below 2^-29 of the largest that its thread block has seen is taken as
  * zero), keys as exact codes and values as fp16; statistics and sums are fp32.  The other
  * arguments are those of kv4_decode_attn.  Three launches: prefix, own positions, merge.
+ * It pays where groups have many rows and prefixes are long: with 32 + 8 heads of 128, groups of 16
+ * and more rows from about 256 K positions attended by the batch in all, groups of 4 from about a
+ * million.  Groups of 2 and 3 rows, and smaller batches, are faster through kv4_decode_attn.
  */
 kv4_status kv4_decode_shared_workspace_bytes(const kv4_cache* cache, int B, int n_groups, size_t* bytes);
 kv4_status kv4_decode_attn_shared(kv4_cache* cache, int layer, int B, const void* q, kv4_dtype q_dtype,

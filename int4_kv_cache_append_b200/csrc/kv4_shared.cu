@@ -19,11 +19,15 @@
 // 15 (P then stays inside fp16): the first unit of a segment sets it, later ones seldom rescale O.
 //
 // What bounds it: 16 prompts of up to 8 K positions with up to 16 answers each, 32 + 8 heads of 128,
-// take 147 us (one by one the prefix kernel 107, own positions 37, merge 10) for 217 MB that have to be
-// read, 33 us at copy speed; one prompt of 16 K with 128 answers 142 us for 35 GFLOP.  A unit of 64
+// take 147 us (one by one the prefix kernel 111, own positions 39, merge 11) for 217 MB that have to be
+// read, 33 us at copy speed; one prompt of 16 K with 128 answers 143 us for 35 GFLOP.  A unit of 64
 // rows takes a CTA about 3200 cycles: the tensor pipe is 16% active, 58% of the issue slots are taken,
-// and a warp issues every seventh cycle, its waits being the fixed latencies of the softmax chain
-// (TMEM load, two packed FMAs, exp2, conversion, store) and the hand-overs between roles.  Eight
+// and a warp issues every eleventh cycle, its waits being the fixed latencies of the softmax chain
+// (TMEM load, two packed FMAs, exp2, conversion, store) and the hand-overs between roles: all 16 softmax
+// warps work on the same unit at the same time.  A group of more than 64 query rows unpacks its pages once
+// for every 64.  It pays for groups of 16 rows from about 256 K attended positions in all, of 4 from a
+// million; else kv4_decode_attn is faster, since rows that share pages find them in L2 (64 rows over 8 K
+// positions each, as groups of 2, 4, 16 and 64: 194, 122, 87, 87 us here, 116 there).  Eight
 // softmax warps of 32 columns, with more registers each, took 165 us where sixteen of 16 took 157.
 #include "kv4_decode_kernel.cuh"
 #include "kv4_quant.cuh"
