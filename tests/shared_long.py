@@ -7,7 +7,6 @@ are those of test_gpu_shared.py, on the dequantised cache, for any queries."""
 import numpy as np
 import torch
 
-from int4_kv_cache_append_b200 import kv4
 from oracle import oracle as O
 
 UNIT = 128  # positions of a unit
@@ -79,8 +78,9 @@ def batch(D, G, Hkv, P, s, w, h, sizes, prefix, past, seed=0, edit=None, ends_di
     return r
 
 
-def to_gpu(r, max_seqs=None):
-    r.cache = kv4.Cache(kv4.Geometry(1, r.Hq, r.Hkv, r.D, r.P, r.s, r.w, r.h, max_seqs or r.B, r.pages), fill=0xA5)
+def to_gpu(r):
+    from int4_kv_cache_append_b200 import kv4
+    r.cache = kv4.Cache(kv4.Geometry(1, r.Hq, r.Hkv, r.D, r.P, r.s, r.w, r.h, r.B, r.pages), fill=0xA5)
     pool, side = r.cache.layer_views(0)
     pool.copy_(torch.from_numpy(r.pool))
     n = min(side.numel(), r.side.size)
